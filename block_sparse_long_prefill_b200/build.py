@@ -9,8 +9,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoba.so")
-SOURCES = ["api.cu", "select.cu", "gate.cu", "attn.cu", "merge.cu", "noalloc.cu", "bwd.cu"]
-HEADERS = ["common.cuh", "params.h", "lists.cuh"]
+SOURCES = ["api.cu", "select.cu", "gate.cu", "attn.cu", "merge.cu", "noalloc.cu", "bwd.cu",
+           "swa_bwd.cu", "rope.cu", "decode.cu"]
+HEADERS = ["common.cuh", "params.h", "lists.cuh", "rows.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -35,6 +35,12 @@ cudaError_t launch_merge(const MergeParams &p, cudaStream_t st);
 int query_major_units(int batch, int hq, int hkv, int block, int is_moba, int row_begin,
                       int row_end);
 cudaError_t launch_bwd(const CUtensorMap *maps, const BwdParams &p, int nsm, cudaStream_t st);
+cudaError_t launch_swa_bwd(const CUtensorMap *maps, const SwaBwdParams &p, int nsm, cudaStream_t st);
+cudaError_t launch_rope_fwd(const RopeParams &p, int d, cudaStream_t st);
+cudaError_t launch_rope_bwd(const RopeParams &p, int d, int grid, cudaStream_t st);
+int rope_bwd_ctas(int batch, int hq, int hkv, int N, int d);
+cudaError_t launch_append(const AppendParams &p, int d, cudaStream_t st);
+cudaError_t launch_decode(const DecodeParams &p, int d, int ctas, cudaStream_t st);
 
 namespace {
 
@@ -186,6 +192,59 @@ int make_kbar_maps(CUtensorMap *maps, const void *split, int batch, int hkv, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return MOBA_ERR_LAUNCH;
   }
+  return MOBA_OK;
+}
+
+// No two elements of an output may share an address through a zero stride.
+bool writable(const moba_tensor &t, int n0, int n1, int n2) {
+  return (n0 == 1 || t.sb > 0) && (n1 == 1 || t.sh > 0) && (n2 == 1 || t.sn > 0);
+}
+
+RopeTensor rope_tensor(const moba_tensor &t) {
+  return RopeTensor{static_cast<uint16_t *>(t.ptr), t.sb, t.sh, t.sn};
+}
+
+int check_swa_bwd(int batch, int hq, int hkv, int N, int d, int window, int sink) {
+  if (batch < 1 || hq < 1 || hkv < 1 || N < 1 || hq % hkv) return MOBA_ERR_SHAPE;
+  if (window < 1 || sink < 0) return MOBA_ERR_ARG;
+  const int rc = check_attn_dim(d);
+  if (rc) return rc;
+  // Row tiles of all heads, and a KV head's walk, are counted in 32 bits.
+  if ((long long)batch * hq * (N / kTileRows + 1) >= (1ll << 30) || N >= (1 << 30)) return MOBA_ERR_SHAPE;
+  return MOBA_OK;
+}
+
+int check_weights(const moba_weight &q, const moba_weight &k, float eps) {
+  for (const moba_weight &w : {q, k}) {
+    if (w.f32 != 0 && w.f32 != 1) return MOBA_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(w.ptr) & (w.f32 ? 3u : 1u)) return MOBA_ERR_ALIGN;
+  }
+  return eps >= 0.f ? MOBA_OK : MOBA_ERR_ARG;   // (false for NaN)
+}
+
+int check_rope(const float *cosp, const float *sinp, const int32_t *positions, const moba_weight &qw,
+               const moba_weight &kw, int batch, int hq, int hkv, int N, int d, int rot, int max_pos,
+               int interleaved, float eps) {
+  if (batch < 1 || hq < 1 || hkv < 1 || N < 1 || max_pos < 1) return MOBA_ERR_SHAPE;
+  // Row groups of all heads are counted as blocks of one grid dimension.
+  if ((double)batch * N * ((double)hq + hkv) >= 8.0 * 2147483647.0) return MOBA_ERR_SHAPE;
+  int rc = check_attn_dim(d);
+  if (rc) return rc;
+  if (rot < 16 || rot > d || rot % 16) return MOBA_ERR_DIM;
+  if (!cosp || !sinp) return MOBA_ERR_ARG;
+  if (!aligned16(cosp) || !aligned16(sinp) || (reinterpret_cast<uintptr_t>(positions) & 3u)) return MOBA_ERR_ALIGN;
+  if (!positions && max_pos < N) return MOBA_ERR_SHAPE;
+  if (interleaved != 0 && interleaved != 1) return MOBA_ERR_ARG;
+  return check_weights(qw, kw, eps);
+}
+
+int check_pages(const moba_tensor &kp, const moba_tensor &vp, const int32_t *table, const int32_t *lens,
+                int batch, int hkv, int page, int num_pages, int max_pages) {
+  if (batch < 1 || hkv < 1 || page < 1 || num_pages < 1 || max_pages < 1) return MOBA_ERR_SHAPE;
+  int rc;
+  if ((rc = check_tensor(kp)) || (rc = check_tensor(vp))) return rc;
+  if (!table || !lens) return MOBA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(table) & 3u) || (reinterpret_cast<uintptr_t>(lens) & 3u)) return MOBA_ERR_ALIGN;
   return MOBA_OK;
 }
 
@@ -517,14 +576,14 @@ int moba_set_pass_events(void *const *events, int count) {
   return MOBA_OK;
 }
 
-int swa_attn_fwd_chunk(moba_tensor q, moba_tensor k, moba_tensor v, int batch, int hq, int hkv,
-                       int N, int Nk, int d, int window, float scale, moba_tensor out, float *lse,
-                       void *stream) {
+int swa_sink_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, int hq, int hkv,
+                      int N, int Nk, int d, int window, int sink, float scale, moba_tensor out,
+                      float *lse, void *stream) {
   if (batch < 1 || hq < 1 || hkv < 1 || N < 1 || hq % hkv) return MOBA_ERR_SHAPE;
   // Query row i sits at key position Nk - N + i (any offset).
   const int q_off = Nk - N;
   if (q_off < 0 || (long long)Nk >= (1ll << 31)) return MOBA_ERR_SHAPE;
-  if (window < 1) return MOBA_ERR_ARG;
+  if (window < 1 || sink < 0) return MOBA_ERR_ARG;
   int rc = check_attn_dim(d);
   if (rc) return rc;
   if ((rc = check_tensor(q)) || (rc = check_tensor(k)) || (rc = check_tensor(v)) ||
@@ -546,6 +605,7 @@ int swa_attn_fwd_chunk(moba_tensor q, moba_tensor k, moba_tensor v, int batch, i
   p.idx = nullptr;
   p.batch = batch; p.hq = hq; p.hkv = hkv; p.N = N; p.d = d; p.block = 0; p.topk = 0;
   p.window = window < Nk ? window : Nk;
+  p.sink = sink < Nk ? sink : Nk;
   p.q_off = q_off;
   p.G = hq / hkv;
   const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
@@ -556,7 +616,14 @@ int swa_attn_fwd_chunk(moba_tensor q, moba_tensor k, moba_tensor v, int batch, i
   p.ntiles = query_major_units(batch, hq, hkv, 0, 0, 0, N);
   p.npast = 0;
   const int grid = p.ntiles < nsm ? p.ntiles : nsm;
-  return launch_status(launch_attn(maps, p, kQueryMajor, grid, static_cast<cudaStream_t>(stream)));
+  return launch_status(launch_attn(maps, p, p.sink > 0 ? kSinkBand : kQueryMajor, grid,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+int swa_attn_fwd_chunk(moba_tensor q, moba_tensor k, moba_tensor v, int batch, int hq, int hkv,
+                       int N, int Nk, int d, int window, float scale, moba_tensor out, float *lse,
+                       void *stream) {
+  return swa_sink_attn_fwd(q, k, v, batch, hq, hkv, N, Nk, d, window, 0, scale, out, lse, stream);
 }
 
 int swa_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, int hq, int hkv, int N,
@@ -631,6 +698,240 @@ int moba_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, 
   return launch_status(launch_bwd(kv, p, nsm, static_cast<cudaStream_t>(stream)));
 }
 
+int swa_bwd_workspace_size(int batch, int hq, int hkv, int N, int d, int window, int sink,
+                           size_t *bytes) {
+  if (!bytes) return MOBA_ERR_ARG;
+  const int rc = check_swa_bwd(batch, hq, hkv, N, d, window, sink);
+  if (rc) return rc;
+  *bytes = swa_bwd_plan(batch, hq, hkv, N, d, window < N ? window : N, sink).total;
+  return MOBA_OK;
+}
+
+int swa_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, moba_tensor dout,
+                 const float *lse, int batch, int hq, int hkv, int N, int d, int window, int sink,
+                 float scale, moba_tensor dq, moba_tensor dk, moba_tensor dv, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+  int rc = check_swa_bwd(batch, hq, hkv, N, d, window, sink);
+  if (rc) return rc;
+  const moba_tensor ts[8] = {q, k, v, out, dout, dq, dk, dv};
+  for (const moba_tensor &t : ts)
+    if ((rc = check_tensor(t))) return rc;
+  if (!writable(dq, batch, hq, N) || !writable(dk, batch, hkv, N) || !writable(dv, batch, hkv, N))
+    return MOBA_ERR_ARG;
+  if (!lse) return MOBA_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOBA_ERR_ALIGN;
+  const int w = window < N ? window : N;
+  const SwaBwdPlan plan = swa_bwd_plan(batch, hq, hkv, N, d, w, sink);
+  if (!workspace || workspace_bytes < plan.total) return MOBA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MOBA_ERR_ALIGN;
+  int nsm = 0;
+  if ((rc = check_device(&nsm))) return rc;
+  CUtensorMap qkv[6], gmaps[6];
+  if ((rc = make_attn_maps(qkv, q, k, v, batch, hq, hkv, N, N, d))) return rc;
+  if ((rc = make_attn_maps(gmaps, dout, k, v, batch, hq, hkv, N, N, d))) return rc;
+  const CUtensorMap maps[8] = {qkv[0], qkv[1], gmaps[0], gmaps[1], qkv[2], qkv[3], qkv[4], qkv[5]};
+  SwaBwdParams p{};
+  if ((rc = status_words(&p.status))) return rc;
+  p.out = static_cast<const uint16_t *>(out.ptr);
+  p.o_sb = out.sb; p.o_sh = out.sh; p.o_sn = out.sn;
+  p.dout = static_cast<const uint16_t *>(dout.ptr);
+  p.do_sb = dout.sb; p.do_sh = dout.sh; p.do_sn = dout.sn;
+  p.lse = lse;
+  p.dq = static_cast<uint16_t *>(dq.ptr);
+  p.dq_sb = dq.sb; p.dq_sh = dq.sh; p.dq_sn = dq.sn;
+  p.dk = static_cast<uint16_t *>(dk.ptr);
+  p.dk_sb = dk.sb; p.dk_sh = dk.sh; p.dk_sn = dk.sn;
+  p.dv = static_cast<uint16_t *>(dv.ptr);
+  p.dv_sb = dv.sb; p.dv_sh = dv.sh; p.dv_sn = dv.sn;
+  char *ws = static_cast<char *>(workspace);
+  p.stat = reinterpret_cast<float *>(ws);
+  p.part = reinterpret_cast<float *>(ws + plan.off_part);
+  p.batch = batch; p.hq = hq; p.hkv = hkv; p.N = N; p.d = d;
+  p.window = w;
+  p.sink = sink < N ? sink : N;
+  p.G = hq / hkv;
+  p.nt = plan.nt; p.nst = plan.nst; p.seg = plan.seg; p.nseg = plan.nseg;
+  const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
+  p.scale = sc;
+  p.scale_log2 = sc * 1.4426950408889634f;
+  return launch_status(launch_swa_bwd(maps, p, nsm, static_cast<cudaStream_t>(stream)));
+}
+
+int qk_norm_rope_fwd(moba_tensor q, moba_tensor k, const float *cosp, const float *sinp,
+                     const int32_t *positions, moba_weight q_weight, moba_weight k_weight, int batch,
+                     int hq, int hkv, int N, int d, int rot, int max_pos, int interleaved, float eps,
+                     moba_tensor q_out, moba_tensor k_out, void *stream) {
+  int rc = check_rope(cosp, sinp, positions, q_weight, k_weight, batch, hq, hkv, N, d, rot, max_pos,
+                      interleaved, eps);
+  if (rc) return rc;
+  const moba_tensor ts[4] = {q, k, q_out, k_out};
+  for (const moba_tensor &t : ts)
+    if ((rc = check_tensor(t))) return rc;
+  if (!writable(q_out, batch, hq, N) || !writable(k_out, batch, hkv, N)) return MOBA_ERR_ARG;
+  if ((rc = check_device(nullptr))) return rc;
+  RopeParams p{};
+  if ((rc = status_words(&p.status))) return rc;
+  p.q = rope_tensor(q); p.k = rope_tensor(k);
+  p.qo = rope_tensor(q_out); p.ko = rope_tensor(k_out);
+  p.qw = RopeWeight{q_weight.ptr, q_weight.f32};
+  p.kw = RopeWeight{k_weight.ptr, k_weight.f32};
+  p.cosp = cosp; p.sinp = sinp; p.positions = positions;
+  p.batch = batch; p.hq = hq; p.hkv = hkv; p.N = N;
+  p.rot = rot; p.max_pos = max_pos; p.interleaved = interleaved;
+  p.eps = eps;
+  return launch_status(launch_rope_fwd(p, d, static_cast<cudaStream_t>(stream)));
+}
+
+int qk_norm_rope_bwd_workspace_size(int batch, int hq, int hkv, int N, int d, size_t *bytes) {
+  if (!bytes) return MOBA_ERR_ARG;
+  if (batch < 1 || hq < 1 || hkv < 1 || N < 1) return MOBA_ERR_SHAPE;
+  const int rc = check_attn_dim(d);
+  if (rc) return rc;
+  *bytes = size_t(rope_bwd_ctas(batch, hq, hkv, N, d)) * 2 * d * sizeof(float);
+  return MOBA_OK;
+}
+
+int qk_norm_rope_bwd(moba_tensor dq_out, moba_tensor dk_out, moba_tensor q, moba_tensor k,
+                     const float *cosp, const float *sinp, const int32_t *positions,
+                     moba_weight q_weight, moba_weight k_weight, int batch, int hq, int hkv, int N,
+                     int d, int rot, int max_pos, int interleaved, float eps, moba_tensor dq,
+                     moba_tensor dk, float *dq_weight, float *dk_weight, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  int rc = check_rope(cosp, sinp, positions, q_weight, k_weight, batch, hq, hkv, N, d, rot, max_pos,
+                      interleaved, eps);
+  if (rc) return rc;
+  const moba_tensor ts[4] = {dq_out, dk_out, dq, dk};
+  for (const moba_tensor &t : ts)
+    if ((rc = check_tensor(t))) return rc;
+  if (q_weight.ptr && (rc = check_tensor(q))) return rc;
+  if (k_weight.ptr && (rc = check_tensor(k))) return rc;
+  if (!writable(dq, batch, hq, N) || !writable(dk, batch, hkv, N)) return MOBA_ERR_ARG;
+  if ((q_weight.ptr != nullptr) != (dq_weight != nullptr) || (k_weight.ptr != nullptr) != (dk_weight != nullptr))
+    return MOBA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(dq_weight) & 3u) || (reinterpret_cast<uintptr_t>(dk_weight) & 3u))
+    return MOBA_ERR_ALIGN;
+  const int grid = rope_bwd_ctas(batch, hq, hkv, N, d);
+  if (q_weight.ptr || k_weight.ptr) {
+    if (!workspace || workspace_bytes < size_t(grid) * 2 * d * sizeof(float)) return MOBA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MOBA_ERR_ALIGN;
+  }
+  if ((rc = check_device(nullptr))) return rc;
+  RopeParams p{};
+  if ((rc = status_words(&p.status))) return rc;
+  p.q = rope_tensor(q); p.k = rope_tensor(k);
+  p.gq = rope_tensor(dq_out); p.gk = rope_tensor(dk_out);
+  p.qo = rope_tensor(dq); p.ko = rope_tensor(dk);
+  p.qw = RopeWeight{q_weight.ptr, q_weight.f32};
+  p.kw = RopeWeight{k_weight.ptr, k_weight.f32};
+  p.cosp = cosp; p.sinp = sinp; p.positions = positions;
+  p.batch = batch; p.hq = hq; p.hkv = hkv; p.N = N;
+  p.rot = rot; p.max_pos = max_pos; p.interleaved = interleaved;
+  p.eps = eps;
+  p.dw = static_cast<float *>(workspace);
+  p.dqw = dq_weight; p.dkw = dk_weight;
+  return launch_status(launch_rope_bwd(p, d, grid, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_append(moba_tensor k, moba_tensor v, moba_tensor q, const int32_t *cu_seqlens,
+              const int32_t *seq_lens, const int32_t *page_table, const float *cosp,
+              const float *sinp, moba_weight q_weight, moba_weight k_weight, int batch, int T, int hq,
+              int hkv, int d, int rot, int max_pos, int interleaved, float eps, int page,
+              int num_pages, int max_pages, moba_tensor k_pages, moba_tensor v_pages,
+              moba_tensor q_out, void *stream) {
+  if (T < 0 || hkv < 1 || (q.ptr && hq < 1)) return MOBA_ERR_SHAPE;
+  int rc = check_pages(k_pages, v_pages, page_table, seq_lens, batch, hkv, page, num_pages, max_pages);
+  if (rc) return rc;
+  if (!cu_seqlens && T != batch) return MOBA_ERR_SHAPE;
+  if (cosp || sinp) {
+    if ((rc = check_rope(cosp, sinp, nullptr, q_weight, k_weight, 1, 1, 1, 1, d, rot, max_pos, interleaved, eps)))
+      return rc;
+  } else {
+    if (rot != 0) return MOBA_ERR_ARG;
+    if ((rc = check_attn_dim(d)) || (rc = check_weights(q_weight, k_weight, eps))) return rc;
+  }
+  if (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) return MOBA_ERR_ALIGN;
+  if (T == 0) return MOBA_OK;
+  if ((rc = check_tensor(k)) || (rc = check_tensor(v))) return rc;
+  if (q.ptr) {
+    if ((rc = check_tensor(q)) || (rc = check_tensor(q_out))) return rc;
+    if (!writable(q_out, 1, hq, T)) return MOBA_ERR_ARG;
+  } else if (q_weight.ptr) {
+    return MOBA_ERR_ARG;
+  }
+  if (!writable(k_pages, num_pages, hkv, page) || !writable(v_pages, num_pages, hkv, page)) return MOBA_ERR_ARG;
+  if ((rc = check_device(nullptr))) return rc;
+  AppendParams p{};
+  if ((rc = status_words(&p.status))) return rc;
+  p.q = rope_tensor(q); p.k = rope_tensor(k); p.v = rope_tensor(v);
+  p.qo = rope_tensor(q_out);
+  p.kp = rope_tensor(k_pages); p.vp = rope_tensor(v_pages);
+  p.qw = RopeWeight{q_weight.ptr, q_weight.f32};
+  p.kw = RopeWeight{k_weight.ptr, k_weight.f32};
+  p.cosp = cosp; p.sinp = sinp;
+  p.cu = cu_seqlens; p.seq_lens = seq_lens; p.table = page_table;
+  p.batch = batch; p.T = T; p.hq = hq; p.hkv = hkv;
+  p.rot = rot; p.max_pos = max_pos; p.interleaved = interleaved;
+  p.page = page; p.num_pages = num_pages; p.max_pages = max_pages;
+  p.eps = eps;
+  return launch_status(launch_append(p, d, static_cast<cudaStream_t>(stream)));
+}
+
+int paged_decode_workspace_size(int batch, int hq, int hkv, int d, size_t *bytes) {
+  if (!bytes) return MOBA_ERR_ARG;
+  if (batch < 1 || hq < 1 || hkv < 1 || hq % hkv) return MOBA_ERR_SHAPE;
+  const int rc = check_attn_dim(d);
+  if (rc) return rc;
+  *bytes = decode_workspace_bytes(batch, d, nullptr, nullptr);
+  return MOBA_OK;
+}
+
+int paged_decode_attn(moba_tensor q, moba_tensor k_pages, moba_tensor v_pages,
+                      const int32_t *page_table, const int32_t *seq_lens, int batch, int hq, int hkv,
+                      int d, int page, int num_pages, int max_pages, int window, int sink,
+                      float scale, moba_tensor out, float *lse, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+  if (batch < 1 || hq < 1 || hkv < 1 || hq % hkv) return MOBA_ERR_SHAPE;
+  int rc = check_attn_dim(d);
+  if (rc) return rc;
+  if (window < 0 || sink < 0) return MOBA_ERR_ARG;
+  if ((rc = check_pages(k_pages, v_pages, page_table, seq_lens, batch, hkv, page, num_pages, max_pages)))
+    return rc;
+  if ((rc = check_tensor(q)) || (rc = check_tensor(out))) return rc;
+  if (!writable(out, batch, hq, 1)) return MOBA_ERR_ARG;
+  if (!lse) return MOBA_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOBA_ERR_ALIGN;
+  const int G = hq / hkv, ngrp = (G + kDecodeRows - 1) / kDecodeRows;
+  // Tiles are counted in 32 bits, sequences x items in one grid dimension.
+  const double tiles = (double)batch * hkv * ngrp * ((double)max_pages * page / 16 + 2);
+  if (tiles >= 2147483648.0 || (double)max_pages * page >= 2147483648.0) return MOBA_ERR_SHAPE;
+  size_t off_o = 0, off_l = 0;
+  const size_t need = decode_workspace_bytes(batch, d, &off_o, &off_l);
+  if (!workspace || workspace_bytes < need) return MOBA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MOBA_ERR_ALIGN;
+  int nsm = 0;
+  if ((rc = check_device(&nsm))) return rc;
+  DecodeParams p{};
+  if ((rc = status_words(&p.status))) return rc;
+  p.q = static_cast<const uint16_t *>(q.ptr);
+  p.q_sb = q.sb; p.q_sh = q.sh;
+  p.out = static_cast<uint16_t *>(out.ptr);
+  p.o_sb = out.sb; p.o_sh = out.sh;
+  p.lse = lse;
+  p.kp = rope_tensor(k_pages); p.vp = rope_tensor(v_pages);
+  p.seq_lens = seq_lens; p.table = page_table;
+  p.batch = batch; p.hq = hq; p.hkv = hkv; p.G = G; p.ngrp = ngrp;
+  p.page = page; p.num_pages = num_pages; p.max_pages = max_pages;
+  p.window = window; p.sink = window > 0 ? sink : 0;
+  const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
+  p.scale_log2 = sc * 1.4426950408889634f;
+  char *ws = static_cast<char *>(workspace);
+  p.before = reinterpret_cast<int *>(ws);
+  p.opart = reinterpret_cast<float *>(ws + off_o);
+  p.lpart = reinterpret_cast<float *>(ws + off_l);
+  const int ctas = 2 * nsm < kDecodeCtas ? 2 * nsm : kDecodeCtas;
+  return launch_status(launch_decode(p, d, ctas, static_cast<cudaStream_t>(stream)));
+}
+
 int moba_device_status(void) {
   int v[2] = {MOBA_OK, 0};
   if (cudaDeviceSynchronize() != cudaSuccess) return MOBA_ERR_LAUNCH;
@@ -667,6 +968,7 @@ const char *moba_status_string(int status) {
     case MOBA_ERR_LAUNCH: return "CUDA launch or driver call failed";
     case MOBA_ERR_DEVICE: return "a kernel wait timed out on the device";
     case MOBA_ERR_NODEVICE: return "no sm_100 device is current";
+    case MOBA_ERR_INDEX: return "a position, length or page id in device memory is out of range";
     case MOBA_ERR_TOO_LARGE: return "problem exceeds the 32 MiB static scratch of moba_prefill_static";
   }
   return "unknown status";

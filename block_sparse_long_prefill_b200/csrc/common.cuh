@@ -42,6 +42,12 @@ __device__ __forceinline__ void record_device_error(int *status, int site) {
   if (atomicCAS(&status[0], MOBA_OK, MOBA_ERR_DEVICE) == MOBA_OK) atomicExch(&status[1], site);
 }
 
+// An index in device memory (a position, a page id, a length) is out of range: the access
+// it names is left out.
+__device__ __forceinline__ void record_index_error(int *status, int site) {
+  if (atomicCAS(&status[0], MOBA_OK, MOBA_ERR_INDEX) == MOBA_OK) atomicExch(&status[1], site);
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {

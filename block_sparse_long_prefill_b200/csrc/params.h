@@ -127,6 +127,7 @@ struct ScatterParams {
 enum AttnMode : int {
   kQueryMajor = 0,  // contiguous 128-row query tiles: own block (MoBA) or band (SWA)
   kGathered = 1,    // gathered rows of one block-major list against one whole block
+  kSinkBand = 2,    // contiguous tiles: band (SWA) and the first keys (sinks)
 };
 
 struct AttnParams {
@@ -141,6 +142,7 @@ struct AttnParams {
   // Problem: N query rows; keys and values run over q_off + N positions, query row i
   // sits at position q_off + i.
   int batch, hq, hkv, N, d, block, topk, window, G;
+  int sink;                // kSinkBand: keys [0, sink) stay visible behind the window
   int q_off;
   float scale_log2;        // scale * log2(e)
   int is_moba;             // 0: sliding window only (swa_attn_fwd)
@@ -197,6 +199,146 @@ inline size_t bwd_workspace_bytes(int batch, int hq, int N, int d, int topk, siz
   const size_t a = align_up(rows * 8, 256);
   if (off_dqp) *off_dqp = a;
   return a + align_up(rows * size_t(topk) * size_t(d) * 4, 256);
+}
+
+constexpr int kRopeBwdCtas = 592;  // most CTAs (partial weight-gradient rows) of the norm + rotary backward
+
+// Parameters of the per-head norm + rotary kernels (rope.cu).  Rows are (b, head, n);
+// strides in elements.
+struct RopeTensor {
+  uint16_t *ptr;           // bf16 bits
+  int64_t sb, sh, sn;
+};
+
+// A per-head weight of D values, bf16 or float32 (null: no norm).
+struct RopeWeight {
+  const void *ptr;
+  int f32;
+};
+
+struct RopeParams {
+  int *status;
+  RopeTensor q, k;         // inputs (the forward's x)
+  RopeTensor qo, ko;       // outputs: the rotated rows, or (backward) dq, dk
+  RopeTensor gq, gk;       // backward: upstream gradients of the rotated rows
+  RopeWeight qw, kw;
+  const float *cosp, *sinp;  // [max_pos, rot / 2]
+  const int32_t *positions;  // [batch, N], or null: position n
+  int batch, hq, hkv, N;
+  int rot, max_pos, interleaved;
+  float eps;
+  float *dw;               // backward: partial weight gradients [grid, 2, D]
+  float *dqw, *dkw;        // backward: weight gradients [D] (null where there is no norm)
+};
+
+// Parameters of the paged append (rope.cu): tokens t of sequence s are
+// cu[s] .. cu[s + 1] - 1 and sit at the last positions below seq_lens[s].
+struct AppendParams {
+  int *status;
+  RopeTensor q, k, v;      // new tokens [T, heads, D] (sb unused); q.ptr may be null
+  RopeTensor qo;           // rotated queries
+  RopeTensor kp, vp;       // pages: sb page, sh KV head, sn slot
+  RopeWeight qw, kw;
+  const float *cosp, *sinp;  // null: no rotation
+  const int32_t *cu;       // [batch + 1], or null: one token per sequence
+  const int32_t *seq_lens; // [batch]
+  const int32_t *table;    // [batch, max_pages]
+  int batch, T, hq, hkv;
+  int rot, max_pos, interleaved;
+  int page, num_pages, max_pages;
+  float eps;
+};
+
+// Parameters of the paged decode (decode.cu).  One query token per sequence, at the last
+// of its seq_lens[b] positions.
+constexpr int kDecodeCtas = 296;      // most CTAs of the main kernel (two per SM)
+constexpr int kDecodeRows = 16;       // query heads of one KV head a CTA takes together
+struct DecodeParams {
+  int *status;
+  const uint16_t *q;       // [batch, hq, D]
+  int64_t q_sb, q_sh;
+  uint16_t *out;
+  int64_t o_sb, o_sh;
+  float *lse;              // [batch, hq]
+  RopeTensor kp, vp;       // pages: sb page, sh KV head, sn slot
+  const int32_t *seq_lens; // [batch]
+  const int32_t *table;    // [batch, max_pages]
+  int batch, hq, hkv, G, ngrp;   // ngrp: groups of kDecodeRows query heads per KV head
+  int page, num_pages, max_pages;
+  int window, sink;
+  float scale_log2;
+  // Workspace: tiles before each sequence [batch + 1], then the partial results: per CTA
+  // two slots (its first and its last item) of kDecodeRows rows of D values and their LSE.
+  int *before;
+  float *opart;            // [ctas, 2, kDecodeRows, D]
+  float *lpart;            // [ctas, 2, kDecodeRows]
+};
+
+inline size_t decode_workspace_bytes(int batch, int d, size_t *off_o, size_t *off_l) {
+  size_t off = align_up(sizeof(int) * (size_t(batch) + 1), 256);
+  const size_t rows = size_t(kDecodeCtas) * 2 * kDecodeRows;
+  if (off_o) *off_o = off;
+  off = align_up(off + rows * size_t(d) * 4, 256);
+  if (off_l) *off_l = off;
+  return align_up(off + rows * 4, 256);
+}
+
+// Parameters of the sliding-window backward (swa_bwd.cu).
+struct SwaBwdParams {
+  int *status;
+  const uint16_t *out, *dout;
+  int64_t o_sb, o_sh, o_sn, do_sb, do_sh, do_sn;
+  const float *lse;        // [batch, hq, N] (natural log)
+  uint16_t *dq, *dk, *dv;
+  int64_t dq_sb, dq_sh, dq_sn, dk_sb, dk_sh, dk_sn, dv_sb, dv_sh, dv_sn;
+  float *stat;             // [batch, hq, nt, 2, 128]: -lse * log2(e), -D = -dO . o of a tile's
+                           // rows (behind row N: -inf, 0)
+  float *part;             // dK, dV of the sinks' key tiles in parts:
+                           // [batch, hkv, nst, 1 + nseg, 2, 128, D]
+  int batch, hq, hkv, N, d, window, sink, G;
+  int nt;                  // 128-row tiles of N
+  int nst;                 // key tiles that hold sinks, 0 when no row sees one behind its band
+  int seg, nseg;           // query tiles of a far part, most far parts of a key tile
+  float scale, scale_log2;
+};
+
+// Query tiles of one head that a key tile's band reaches: kt .. swa_last_tile.
+__host__ __device__ inline int swa_last_tile(int kt, int window, int nt) {
+  const long long last = ((long long)kt * kTileKeys + kTileKeys - 1 + window - 1) / kTileRows;
+  return last < nt - 1 ? (int)last : nt - 1;
+}
+
+// Split of the sinks' walks and the workspace of the sliding-window backward.  A key tile
+// with sinks is attended by the query tiles of its band, like every key tile, and by all
+// later ones; these are cut into parts of `seg` query tiles (of all G heads) so that no
+// part is much longer than a band's walk.
+struct SwaBwdPlan {
+  int nt, nst, seg, nseg;
+  size_t off_part, total;
+};
+
+inline SwaBwdPlan swa_bwd_plan(int batch, int hq, int hkv, int N, int d, int window, int sink) {
+  SwaBwdPlan w{};
+  w.nt = (N + kTileRows - 1) / kTileRows;
+  const int G = hq / hkv;
+  const long long far0 = (long long)G * (w.nt - 1 - swa_last_tile(0, window, w.nt));
+  if (sink > 0 && far0 > 0) {
+    const int s = sink < N ? sink : N;
+    w.nst = (s + kTileKeys - 1) / kTileKeys;
+    // At least a band's walk (or 16 tiles) a part, and about eight parts per SM at most.
+    long long seg = (long long)G * (window / kTileRows + 2);
+    if (seg < 16) seg = 16;
+    const long long all = far0 * w.nst * hkv * batch;
+    if (seg < all / 1184) seg = all / 1184;
+    if (seg > far0) seg = far0;
+    w.seg = (int)seg;
+    w.nseg = (int)((far0 + seg - 1) / seg);
+  }
+  size_t off = align_up(size_t(batch) * hq * w.nt * 2 * kTileRows * 4, 1024);
+  w.off_part = off;
+  off += size_t(batch) * hkv * w.nst * (1 + w.nseg) * 2 * kTileKeys * d * 4;
+  w.total = align_up(off, 256);
+  return w;
 }
 
 }  // namespace moba

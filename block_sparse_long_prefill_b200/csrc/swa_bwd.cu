@@ -1,0 +1,845 @@
+// swa_bwd.cu -- backward of sliding-window attention with sinks on sm_100a tensor cores.
+//
+// [SWA] = "SWA + MoE: 어텐션과 희소 전문가", Bit-Axon architecture page (§"어텐션 공식",
+//         §"슬라이딩 윈도우 마스크").
+//
+// Row i attends the keys j <= i with i - j < window or j < sink.  With z_ij = scale q_i.k_j,
+// p_ij = exp(z_ij - lse_i) and the upstream gradient dO:
+//     D_i = dO_i . o_i,  dz_ij = p_ij (dO_i . v_j - D_i)
+//     dQ_i = scale sum_j dz_ij k_j,  dK_j = scale sum_i dz_ij q_i,  dV_j = sum_i p_ij dO_i
+// (a KV head's dK and dV sum over the q-heads that read it).  No atomics: every sum has one
+// order, so results repeat bit for bit.
+//
+//   swa_bwd_prep_kernel   per row -lse log2(e) and -D, in the tiles' order; HBM-bound
+//   swa_bwd_dq_kernel     query-stationary: a 128-row tile walks its key chunks (the sinks'
+//                         chunks before the band, then the band): S = Q K^T, dP = dO V^T,
+//                         dS = P (dP - D) on the CUDA cores, dQ += dS K in TMEM; written once
+//   swa_bwd_dkdv_kernel   key-stationary: a 128-key tile walks the query tiles that attend
+//                         it, of every q-head of its group: S^T = K Q^T, dP^T = V dO^T,
+//                         dV += P^T dO, dK += dS^T Q in TMEM; written once.  The sinks' key
+//                         tiles are attended by every later row, a walk up to N / window
+//                         times as long, so theirs are cut into parts that leave fp32 sums
+//   swa_bwd_join_kernel   adds the parts of the sinks' key tiles
+//
+// Both tile kernels compute S and dP again (7 products instead of 5): a single pass would
+// have to add dQ in global memory from every key tile, in an order that varies.  They are
+// bound by the CUDA cores: per 128 x 128 tile 16384 exponentials at 16 a cycle are 1024
+// cycles, against 768 (dQ) or 1024 (dK, dV) cycles of products at D = 128.  So the
+// elementwise work goes in two groups of four warps, each with its half of the columns and
+// its own TMEM buffers, and the steps of consecutive items run on without a gap: the next
+// item's first products are issued before the last item's are summed up.
+//   warp 0      TMA: K, V, and Q with dO (and their row statistics) in rings of their own
+//   warp 1      tcgen05 issuer (one thread) and TMEM owner
+//   warps 2-9   elementwise groups 0 and 1; a thread owns one TMEM lane
+// Every wait is bounded, as in the forward.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "params.h"
+#include "rows.cuh"
+
+namespace moba {
+
+constexpr int kSwaBwdThreads = 320;
+
+// A 128-row tile of D columns: a 64-column region with 128-byte swizzle, then columns
+// [64, 128) the same way (D = 128) or [64, 80) with 32-byte swizzle (D = 80).
+template <int D>
+struct SwaTile {
+  static constexpr int R0 = 128 * 128;
+  static constexpr int R1 = D == 128 ? 128 * 128 : (D == 80 ? 128 * 32 : 0);
+  static constexpr int TILE = R0 + R1;
+  static constexpr uint32_t BYTES = 128u * D * 2u;
+  static_assert(BYTES == (uint32_t)TILE, "a tile is packed");
+};
+
+// K-major operand (rows = M or N), columns [16 ks, 16 ks + 16), from row 64 half on.
+template <int D>
+__device__ __forceinline__ uint64_t swa_kmajor(uint32_t tile, int ks, int half) {
+  if (ks < 4) return smem_desc(tile + half * 8192 + ks * 32, 16, 1024, kSwizzle128);
+  if (D == 128) return smem_desc(tile + SwaTile<D>::R0 + half * 8192 + (ks - 4) * 32, 16, 1024, kSwizzle128);
+  return smem_desc(tile + SwaTile<D>::R0 + half * 2048, 16, 256, kSwizzle32);
+}
+
+// D[tmem, D columns] (+)= A[tmem, 16 columns of K] B[rows 16 kk .. of the tile, D columns].
+template <int D>
+__device__ __forceinline__ void swa_acc(uint32_t d, uint32_t a, uint32_t tile, int kk, uint32_t acc) {
+  if (D == 128) {
+    umma_ts(d, a, smem_desc(tile + kk * 2048, SwaTile<D>::R0, 1024, kSwizzle128),
+            idesc_bf16(128, 128, 0, 1), acc);
+  } else {
+    umma_ts(d, a, smem_desc(tile + kk * 2048, 16, 1024, kSwizzle128), idesc_bf16(128, 64, 0, 1), acc);
+    if (D == 80)
+      umma_ts(d + 64, a, smem_desc(tile + SwaTile<D>::R0 + kk * 512, 16, 256, kSwizzle32),
+              idesc_bf16(128, 16, 0, 1), acc);
+  }
+}
+
+// S_half (64 columns) = A B_half^T over the D columns.
+template <int D>
+__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int half) {
+  constexpr uint32_t id = idesc_bf16(128, 64, 0, 0);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    umma_ss(d, swa_kmajor<D>(a, ks, 0), swa_kmajor<D>(b, ks, half), id, ks > 0 ? 1u : 0u);
+}
+
+template <int D>
+__device__ __forceinline__ void swa_load_tile(unsigned char *dst, const CUtensorMap *m, const CUtensorMap *m1,
+                                              uint64_t *bar, int row, int h, int b) {
+  tma_load_4d(dst, m, bar, 0, row, h, b);
+  if (D != 64) tma_load_4d(dst + SwaTile<D>::R0, m1, bar, 64, row, h, b);
+}
+
+// Bulk copy of a tile's row statistics (1 KB, 16-byte aligned on both sides).
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// After an abort: waits (with the limit) until the last loads of a ring have landed.
+__device__ __forceinline__ void drain_ring(uint64_t *full, uint32_t cnt, uint32_t stages, const int *status) {
+  for (uint32_t u = cnt > stages ? cnt - stages : 0; u < cnt; ++u) {
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(&full[u % stages], (u / stages) & 1) && global_timer_ns() - t0 < wait_limit_ns(status)) {}
+  }
+}
+
+// Packed fp32 pairs, each lane rounded as the scalar instruction would.
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b, float c0, float c1) {
+  asm("{.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+// d = p * (v + c) on pairs.
+__device__ __forceinline__ void addmul2(float &d0, float &d1, float v0, float v1, float c0, float c1,
+                                        float p0, float p1) {
+  asm("{.reg .b64 rv, rc, rp, rd;\n\t"
+      "mov.b64 rv, {%2, %3};\n\tmov.b64 rc, {%4, %5};\n\tmov.b64 rp, {%6, %7};\n\t"
+      "add.rn.f32x2 rd, rv, rc;\n\tmul.rn.f32x2 rd, rd, rp;\n\tmov.b64 {%0, %1}, rd;}"
+      : "=f"(d0), "=f"(d1) : "f"(v0), "f"(v1), "f"(c0), "f"(c1), "f"(p0), "f"(p1));
+}
+
+// ------------------------------------------------------------------ prep
+
+template <int D>
+__global__ void __launch_bounds__(256) swa_bwd_prep_kernel(const SwaBwdParams p) {
+  constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
+  const int lane = threadIdx.x & 31;
+  const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
+  const bool in = v < LPR;
+  const int vv = in ? v : 0;
+  const int padded = p.nt * kTileRows;
+  const int groups = (padded + RPW - 1) / RPW;
+  const long long tasks = (long long)p.batch * p.hq * groups;
+  const long long nw = (long long)gridDim.x * 8;
+  for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < tasks; task += nw) {
+    const long long bh = task / groups;
+    const int i = (int)(task - bh * groups) * RPW + sub;
+    const int b = (int)(bh / p.hq), h = (int)(bh % p.hq);
+    const bool live = in && i < p.N;
+    float acc = 0.f;
+    if (live) {
+      float x[8], g[8];
+      unpack8(__ldg(reinterpret_cast<const uint4 *>(p.out + b * p.o_sb + h * p.o_sh + (int64_t)i * p.o_sn + vv * 8)), x);
+      unpack8(__ldg(reinterpret_cast<const uint4 *>(p.dout + b * p.do_sb + h * p.do_sh + (int64_t)i * p.do_sn + vv * 8)), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc = fmaf(x[e], g[e], acc);
+    }
+    acc = row_sum<D>(acc, base, vv);
+    if (in && v == 0 && i < padded) {
+      float *st = p.stat + (bh * p.nt + i / kTileRows) * 256 + (i & 127);
+      st[0] = live ? -p.lse[bh * p.N + i] * 1.4426950408889634f : -INFINITY;
+      st[128] = live ? -acc : 0.f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+
+// Work item u: one 128-row query tile; its key chunks: ns chunks of sinks from key 0, then
+// the band's from chunk c0.
+struct SwaDqItem {
+  int b, h, hk, qt, ns, c0, nc;
+};
+
+__device__ __forceinline__ SwaDqItem swa_dq_item(const SwaBwdParams &p, int u) {
+  SwaDqItem w;
+  w.qt = p.nt - 1 - u % p.nt;                    // later (longer) walks first
+  const int bh = u / p.nt;
+  w.b = bh / p.hq;
+  w.h = bh % p.hq;
+  w.hk = w.h / p.G;
+  w.c0 = max(0, w.qt * kTileRows - p.window + 1) / kTileKeys;
+  w.ns = min((p.sink + kTileKeys - 1) / kTileKeys, w.c0);
+  w.nc = w.ns + w.qt - w.c0 + 1;
+  return w;
+}
+
+__device__ __forceinline__ int swa_dq_key(const SwaDqItem &w, int m) {
+  return (m < w.ns ? m : w.c0 + m - w.ns) * kTileKeys;
+}
+
+template <int D>
+struct SwaDqCfg {
+  static constexpr int QS = D == 128 ? 1 : 2;              // Q / dO stages
+  static constexpr int ST = D == 128 ? 2 : (D == 80 ? 3 : 4);  // K and V stages
+  static constexpr int Q_OFF = 0;
+  static constexpr int DO_OFF = QS * SwaTile<D>::TILE;
+  static constexpr int K_OFF = 2 * QS * SwaTile<D>::TILE;
+  static constexpr int V_OFF = K_OFF + ST * SwaTile<D>::TILE;
+  static constexpr int BAR_OFF = V_OFF + ST * SwaTile<D>::TILE;
+  static constexpr int SMEM = BAR_OFF + 1024 + 1024;
+};
+
+struct SwaBars {
+  uint64_t q_full[4], q_empty[4];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], ds_full[2];      // per group: products ready; dS (and P) written back
+  uint64_t acc_full[2], acc_empty[2];  // accumulators final / read out
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void swa_init_bars(SwaBars &bar) {
+  for (int s = 0; s < 4; ++s) {
+    mbar_init(&bar.q_full[s], 1);
+    mbar_init(&bar.q_empty[s], 1);
+    mbar_init(&bar.k_full[s], 1);
+    mbar_init(&bar.k_empty[s], 1);
+    mbar_init(&bar.v_full[s], 1);
+    mbar_init(&bar.v_empty[s], 1);
+  }
+  for (int x = 0; x < 2; ++x) {
+    mbar_init(&bar.s_full[x], 1);
+    mbar_init(&bar.ds_full[x], 128);
+    mbar_init(&bar.acc_full[x], 1);
+    mbar_init(&bar.acc_empty[x], 256);
+  }
+  mbar_init(&bar.mma_done, 1);
+  bar.abort = 0;
+  fence_barrier_init();
+}
+
+// 16 columns of accumulators, scaled, as bf16 to a row.
+__device__ __forceinline__ void store16(uint16_t *dst, const uint32_t (&o)[16], float sc) {
+#pragma unroll
+  for (int e = 0; e < 16; e += 8) {
+    uint4 x;
+    x.x = pack_bf16x2(__uint_as_float(o[e]) * sc, __uint_as_float(o[e + 1]) * sc);
+    x.y = pack_bf16x2(__uint_as_float(o[e + 2]) * sc, __uint_as_float(o[e + 3]) * sc);
+    x.z = pack_bf16x2(__uint_as_float(o[e + 4]) * sc, __uint_as_float(o[e + 5]) * sc);
+    x.w = pack_bf16x2(__uint_as_float(o[e + 6]) * sc, __uint_as_float(o[e + 7]) * sc);
+    *reinterpret_cast<uint4 *>(dst + e) = x;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSwaBwdThreads, 1)
+swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
+                  const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG1,
+                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV1,
+                  const SwaBwdParams p) {
+  using C = SwaDqCfg<D>;
+  using T = SwaTile<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char *sbase = smem_raw + (base - raw);
+  SwaBars &bar = *reinterpret_cast<SwaBars *>(sbase + C::BAR_OFF);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int site0 = (40 * 16 + (D == 64 ? 0 : (D == 80 ? 1 : 2))) * 256;
+  constexpr uint32_t FULL = 0xffffffffu;
+  const int nitems = p.batch * p.hq * p.nt;
+
+  if (tid == 0) swa_init_bars(bar);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmG);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_base;
+  volatile int *abort = &bar.abort;
+  // TMEM: S_x at 128 x, dP_x at 128 x + 64 (x: column half and group); dQ at 256 and 384.
+
+  if (warp == 0) {
+    if (lane < 2) {
+      // ---------------------------------------------------------- K (lane 0), V (lane 1)
+      const bool kside = lane == 0;
+      uint64_t *full = kside ? bar.k_full : bar.v_full;
+      uint64_t *empty = kside ? bar.k_empty : bar.v_empty;
+      const CUtensorMap *m0 = kside ? &tmK : &tmV, *m1 = kside ? &tmK1 : &tmV1;
+      unsigned char *ring = sbase + (kside ? C::K_OFF : C::V_OFF);
+      uint32_t cnt = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
+        const SwaDqItem w = swa_dq_item(p, u);
+        for (int m = 0; m < w.nc; ++m, ++cnt) {
+          const uint32_t st = cnt % C::ST;
+          if (!(ok = mbar_wait(&empty[st], ((cnt / C::ST) & 1) ^ 1, abort, p.status, site0 + 1))) break;
+          mbar_arrive_expect_tx(&full[st], T::BYTES);
+          swa_load_tile<D>(ring + st * T::TILE, m0, m1, &full[st], swa_dq_key(w, m), w.hk, w.b);
+        }
+      }
+      if (*abort) drain_ring(full, cnt, C::ST, p.status);
+    } else if (lane == 2) {
+      // ---------------------------------------------------------- Q and dO
+      uint32_t cnt = 0;
+      for (int u = blockIdx.x; u < nitems; u += gridDim.x, ++cnt) {
+        const SwaDqItem w = swa_dq_item(p, u);
+        const uint32_t st = cnt % C::QS;
+        if (!mbar_wait(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2)) break;
+        mbar_arrive_expect_tx(&bar.q_full[st], 2 * T::BYTES);
+        swa_load_tile<D>(sbase + C::Q_OFF + st * T::TILE, &tmQ, &tmQ1, &bar.q_full[st], w.qt * kTileRows, w.h, w.b);
+        swa_load_tile<D>(sbase + C::DO_OFF + st * T::TILE, &tmG, &tmG1, &bar.q_full[st], w.qt * kTileRows, w.h, w.b);
+      }
+      if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      // Step by step over the chunks of all items: per half x, dQ += dS_x K_x of the last
+      // step (once group x has written dS over S_x), then S_x and dP_x of this step.
+      uint32_t step = 0, qn = 0, an = 0;   // steps, items begun, items whose dQ began
+      uint32_t sc[2] = {0u, 0u};
+      bool ok = true;
+      int u = blockIdx.x, m = 0;
+      SwaDqItem w{};
+      if (u < nitems) w = swa_dq_item(p, u);
+      bool prev = false, prev_first = false, prev_last = false;
+      while (ok && (u < nitems || prev)) {
+        const bool cur = u < nitems;
+        const uint32_t st = step % C::ST, pst = (step - 1) % C::ST;
+        const uint32_t qs = qn % C::QS;
+        if (cur) {
+          if (m == 0 && !(ok = mbar_wait(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
+          if (!(ok = mbar_wait(&bar.k_full[st], (step / C::ST) & 1, abort, p.status, site0 + 4))) break;
+          if (!(ok = mbar_wait(&bar.v_full[st], (step / C::ST) & 1, abort, p.status, site0 + 5))) break;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t tS = tmem + 128 * x, tP = tS + 64;
+          if (prev) {
+            if (!(ok = mbar_wait(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 6))) break;
+            ++sc[x];
+            if (x == 0 && prev_first) {
+              if (!(ok = mbar_wait(&bar.acc_empty[an & 1], ((an >> 1) & 1) ^ 1, abort, p.status, site0 + 7))) break;
+              ++an;
+            }
+            tc_fence_after();
+            const uint32_t kt = base + C::K_OFF + pst * T::TILE;
+            const uint32_t tQ = tmem + 256 + 128 * ((an - 1) & 1);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              swa_acc<D>(tQ, tS + kk * 8, kt, 4 * x + kk, (prev_first && x == 0 && kk == 0) ? 0u : 1u);
+            if (x == 1) {
+              umma_commit(&bar.k_empty[pst]);
+              if (prev_last) umma_commit(&bar.acc_full[(an - 1) & 1]);
+            }
+          }
+          if (cur) {
+            const uint32_t qt = base + C::Q_OFF + qs * T::TILE, gt = base + C::DO_OFF + qs * T::TILE;
+            swa_scores<D>(tS, qt, base + C::K_OFF + st * T::TILE, x);
+            swa_scores<D>(tP, gt, base + C::V_OFF + st * T::TILE, x);
+            umma_commit(&bar.s_full[x]);
+            if (x == 1) {
+              umma_commit(&bar.v_empty[st]);
+              if (m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
+            }
+          }
+        }
+        if (!ok) break;
+        prev = cur;
+        if (cur) {
+          prev_first = m == 0;
+          prev_last = m == w.nc - 1;
+          ++step;
+          if (++m == w.nc) {
+            ++qn;
+            m = 0;
+            u += gridDim.x;
+            if (u < nitems) w = swa_dq_item(p, u);
+          }
+        }
+      }
+      umma_commit(&bar.mma_done);
+      const unsigned long long t0 = global_timer_ns();
+      while (!mbar_try_wait(&bar.mma_done, 0) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
+    }
+  } else {
+    // ------------------------------------------------------------ dS, and dQ out
+    const int q4 = warp & 3, grp = (warp - 2) >> 2;
+    const int r = 32 * q4 + lane;                   // row == TMEM lane
+    const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+    const uint32_t tS = tmem + lane_off + 128 * grp, tP = tS + 64;
+    const float sl2 = p.scale_log2;
+    uint32_t sc = 0, an = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
+      const SwaDqItem w = swa_dq_item(p, u);
+      const int i0 = w.qt * kTileRows, i = i0 + r;
+      const float *st = p.stat + (((int64_t)w.b * p.hq + w.h) * p.nt + w.qt) * 256 + r;
+      const float nl = st[0], nd = st[128];
+      for (int m = 0; m < w.nc; ++m, ++sc) {
+        ok = mbar_wait(&bar.s_full[grp], sc & 1, abort, p.status, site0 + 8);
+        if (!(ok = __all_sync(FULL, ok))) break;
+        tc_fence_after();
+        const int key0 = swa_dq_key(w, m) + 64 * grp;
+        const bool full = key0 + 63 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 64 <= p.sink);
+        uint32_t sv[64], pv[64];
+        tmem_ld64(tS, sv);
+        tmem_ld64(tP, pv);
+        tmem_wait_ld();
+        uint32_t ds[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          float x0, x1, d0, d1;
+          fma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, nl, nl);
+          addmul2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), nd, nd, ex2_approx(x0), ex2_approx(x1));
+          if (!full) {
+            const int k0 = key0 + e, k1 = k0 + 1;
+            if (k0 > i || (i - k0 >= p.window && k0 >= p.sink)) d0 = 0.f;
+            if (k1 > i || (i - k1 >= p.window && k1 >= p.sink)) d1 = 0.f;
+          }
+          ds[e / 2] = pack_bf16x2(d0, d1);
+        }
+        tmem_st32(tS, ds);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.ds_full[grp]);
+      }
+      if (!ok) break;
+      ok = mbar_wait(&bar.acc_full[an & 1], (an >> 1) & 1, abort, p.status, site0 + 9);
+      if (!(ok = __all_sync(FULL, ok))) break;
+      tc_fence_after();
+      // A lane's 16 columns are one whole 32-byte sector of its row.
+      uint16_t *dst = p.dq + (int64_t)w.b * p.dq_sb + (int64_t)w.h * p.dq_sh + (int64_t)i * p.dq_sn;
+      constexpr int CUT = D == 80 ? 48 : D / 2;     // columns of group 0
+      const uint32_t tQ = tmem + lane_off + 256 + 128 * (an & 1);
+      ++an;
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        if ((c < CUT) != (grp == 0)) continue;
+        uint32_t o[16];
+        tmem_ld16(tQ + c, o);
+        tmem_wait_ld();
+        if (i < p.N) store16(dst + c, o, p.scale);
+      }
+      tc_fence_before();
+      mbar_arrive(&bar.acc_empty[(an - 1) & 1]);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ dK / dV
+
+// Unit u: first the far parts of the sinks' key tiles (the longest walks), then every key
+// tile's band.  Its walk: entries t0 .. t1 - 1 of the list of `len` query tiles from `first`
+// on, head after head.
+struct SwaDkvUnit {
+  int b, hk, kt;
+  int first, len, t0, t1;
+  int part;        // -1: the gradients themselves; else the part they are a sum of
+};
+
+__device__ __forceinline__ int swa_dkv_units(const SwaBwdParams &p) {
+  return p.batch * p.hkv * (p.nst * p.nseg + p.nt);
+}
+
+__device__ __forceinline__ bool swa_dkv_unit(const SwaBwdParams &p, int u, SwaDkvUnit &w) {
+  const int heads = p.batch * p.hkv, nfar = heads * p.nst * p.nseg;
+  int seg = -1;
+  if (u < nfar) {
+    seg = u / (heads * p.nst);
+    const int rest = u - seg * heads * p.nst;
+    w.kt = rest / heads;
+    u = rest - w.kt * heads;
+  } else {
+    u -= nfar;
+    w.kt = u / heads;
+    u -= w.kt * heads;
+  }
+  w.b = u / p.hkv;
+  w.hk = u - w.b * p.hkv;
+  const int last = swa_last_tile(w.kt, p.window, p.nt);
+  const int far = p.nt - 1 - last;
+  if (seg >= 0) {
+    w.first = last + 1;
+    w.len = far;
+    w.t0 = seg * p.seg;
+    w.t1 = min(w.t0 + p.seg, p.G * far);
+    w.part = 1 + seg;
+  } else {
+    w.first = w.kt;
+    w.len = last - w.kt + 1;
+    w.t0 = 0;
+    w.t1 = p.G * w.len;
+    w.part = (w.kt < p.nst && far > 0) ? 0 : -1;
+  }
+  return w.t0 < w.t1;
+}
+
+template <int D>
+struct SwaDkvCfg {
+  static constexpr int KS = D == 128 ? 1 : 2;                  // K / V stages
+  static constexpr int QS = D == 128 ? 2 : (D == 80 ? 3 : 4);  // Q / dO / statistics stages
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = KS * SwaTile<D>::TILE;
+  static constexpr int Q_OFF = 2 * KS * SwaTile<D>::TILE;
+  static constexpr int DO_OFF = Q_OFF + QS * SwaTile<D>::TILE;
+  static constexpr int ST_OFF = DO_OFF + QS * SwaTile<D>::TILE;
+  static constexpr int BAR_OFF = ST_OFF + QS * 1024;
+  static constexpr int SMEM = BAR_OFF + 1024 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kSwaBwdThreads, 1)
+swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
+                    const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG1,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV1,
+                    const SwaBwdParams p) {
+  using C = SwaDkvCfg<D>;
+  using T = SwaTile<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char *sbase = smem_raw + (base - raw);
+  SwaBars &bar = *reinterpret_cast<SwaBars *>(sbase + C::BAR_OFF);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int site0 = (41 * 16 + (D == 64 ? 0 : (D == 80 ? 1 : 2))) * 256;
+  constexpr uint32_t FULL = 0xffffffffu;
+  const int nunits = swa_dkv_units(p);
+
+  if (tid == 0) swa_init_bars(bar);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmG);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_base;
+  volatile int *abort = &bar.abort;
+  // TMEM: S^T_x at 128 x, dP^T_x at 128 x + 64 (x: query half and group); dK at 256, dV at
+  // 256 + D.
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- K and V
+      uint32_t cnt = 0;
+      for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
+        SwaDkvUnit w;
+        if (!swa_dkv_unit(p, u, w)) continue;
+        const uint32_t st = cnt % C::KS;
+        if (!mbar_wait(&bar.k_empty[st], ((cnt / C::KS) & 1) ^ 1, abort, p.status, site0 + 1)) break;
+        mbar_arrive_expect_tx(&bar.k_full[st], 2 * T::BYTES);
+        swa_load_tile<D>(sbase + C::K_OFF + st * T::TILE, &tmK, &tmK1, &bar.k_full[st], w.kt * kTileKeys, w.hk, w.b);
+        swa_load_tile<D>(sbase + C::V_OFF + st * T::TILE, &tmV, &tmV1, &bar.k_full[st], w.kt * kTileKeys, w.hk, w.b);
+        ++cnt;
+      }
+      if (*abort) drain_ring(bar.k_full, cnt, C::KS, p.status);
+    } else if (lane == 1) {
+      // ---------------------------------------------------------- Q, dO, row statistics
+      uint32_t cnt = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
+        SwaDkvUnit w;
+        if (!swa_dkv_unit(p, u, w)) continue;
+        int g = w.t0 / w.len, qt = w.first + w.t0 % w.len;
+        for (int t = w.t0; t < w.t1; ++t, ++cnt) {
+          const uint32_t st = cnt % C::QS;
+          if (!(ok = mbar_wait(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2))) break;
+          const int h = w.hk * p.G + g;
+          mbar_arrive_expect_tx(&bar.q_full[st], 2 * T::BYTES + 1024);
+          swa_load_tile<D>(sbase + C::Q_OFF + st * T::TILE, &tmQ, &tmQ1, &bar.q_full[st], qt * kTileRows, h, w.b);
+          swa_load_tile<D>(sbase + C::DO_OFF + st * T::TILE, &tmG, &tmG1, &bar.q_full[st], qt * kTileRows, h, w.b);
+          bulk_load(sbase + C::ST_OFF + st * 1024, p.stat + (((int64_t)w.b * p.hq + h) * p.nt + qt) * 256, 1024,
+                    &bar.q_full[st]);
+          if (++qt == w.first + w.len) {
+            qt = w.first;
+            ++g;
+          }
+        }
+      }
+      if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      // Step by step over the query tiles of all units: per half x, dV += P^T_x dO_x and
+      // dK += dS^T_x Q_x of the last step, then S^T_x and dP^T_x of this step.
+      uint32_t step = 0, kn = 0, an = 0;
+      uint32_t sc[2] = {0u, 0u};
+      bool ok = true;
+      SwaDkvUnit w{};
+      auto seek = [&](int v) {
+        while (v < nunits && !swa_dkv_unit(p, v, w)) v += gridDim.x;
+        return v;
+      };
+      int u = seek(blockIdx.x), t = w.t0;
+      bool prev = false, prev_first = false, prev_last = false;
+      const uint32_t tK = tmem + 256, tV = tmem + 256 + D;
+      while (ok && (u < nunits || prev)) {
+        const bool cur = u < nunits;
+        const uint32_t st = step % C::QS, pst = (step - 1) % C::QS, ks = kn % C::KS;
+        const bool last = t == w.t1 - 1;
+        if (cur) {
+          if (t == w.t0 && !(ok = mbar_wait(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3))) break;
+          if (!(ok = mbar_wait(&bar.q_full[st], (step / C::QS) & 1, abort, p.status, site0 + 4))) break;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t tS = tmem + 128 * x, tP = tS + 64;
+          if (prev) {
+            if (!(ok = mbar_wait(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 5))) break;
+            ++sc[x];
+            if (x == 0 && prev_first) {
+              if (!(ok = mbar_wait(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 6))) break;
+              ++an;
+            }
+            tc_fence_after();
+            const uint32_t qp = base + C::Q_OFF + pst * T::TILE, gp = base + C::DO_OFF + pst * T::TILE;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t acc = (prev_first && x == 0 && kk == 0) ? 0u : 1u;
+              swa_acc<D>(tV, tS + kk * 8, gp, 4 * x + kk, acc);
+              swa_acc<D>(tK, tP + kk * 8, qp, 4 * x + kk, acc);
+            }
+            if (x == 1) {
+              umma_commit(&bar.q_empty[pst]);
+              if (prev_last) umma_commit(&bar.acc_full[0]);
+            }
+          }
+          if (cur) {
+            const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
+            swa_scores<D>(tS, kt, base + C::Q_OFF + st * T::TILE, x);
+            swa_scores<D>(tP, vt, base + C::DO_OFF + st * T::TILE, x);
+            umma_commit(&bar.s_full[x]);
+            if (x == 1 && last) umma_commit(&bar.k_empty[ks]);
+          }
+        }
+        if (!ok) break;
+        prev = cur;
+        if (cur) {
+          prev_first = t == w.t0;
+          prev_last = last;
+          ++step;
+          ++t;
+          if (last) {
+            ++kn;
+            u = seek(u + gridDim.x);
+            t = w.t0;
+          }
+        }
+      }
+      umma_commit(&bar.mma_done);
+      const unsigned long long t0 = global_timer_ns();
+      while (!mbar_try_wait(&bar.mma_done, 0) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
+    }
+  } else {
+    // ------------------------------------------------------------ P^T, dS^T; dK, dV out
+    const int q4 = warp & 3, grp = (warp - 2) >> 2;
+    const int r = 32 * q4 + lane;                   // key of the tile == TMEM lane
+    const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+    const uint32_t tS = tmem + lane_off + 128 * grp, tP = tS + 64;
+    const uint32_t tK = tmem + lane_off + 256, tV = tK + D;
+    const float sl2 = p.scale_log2;
+    uint32_t sc = 0, an = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
+      SwaDkvUnit w;
+      if (!swa_dkv_unit(p, u, w)) continue;
+      const int key0 = w.kt * kTileKeys, key = key0 + r;
+      int qt = w.first + w.t0 % w.len;
+      for (int t = w.t0; t < w.t1; ++t, ++sc) {
+        const uint32_t st = sc % C::QS;
+        ok = mbar_wait(&bar.q_full[st], (sc / C::QS) & 1, abort, p.status, site0 + 7);
+        if (!(ok = __all_sync(FULL, ok))) break;
+        ok = mbar_wait(&bar.s_full[grp], sc & 1, abort, p.status, site0 + 8);
+        if (!(ok = __all_sync(FULL, ok))) break;
+        tc_fence_after();
+        const float *nl = reinterpret_cast<const float *>(sbase + C::ST_OFF + st * 1024) + 64 * grp;
+        const int i0 = qt * kTileRows + 64 * grp;   // row of the group's first column
+        const bool full = key0 + kTileKeys - 1 <= i0 && (i0 + 63 - key0 < p.window || key0 + kTileKeys <= p.sink);
+        if (++qt == w.first + w.len) qt = w.first;
+        uint32_t sv[64], pv[64];
+        tmem_ld64(tS, sv);
+        tmem_ld64(tP, pv);
+        tmem_wait_ld();
+        uint32_t pp[32], dd[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          const float4 l4 = *reinterpret_cast<const float4 *>(nl + e);
+          const float4 d4 = *reinterpret_cast<const float4 *>(nl + 128 + e);
+          float pr[4], ds[4];
+          fma2(pr[0], pr[1], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, l4.x, l4.y);
+          fma2(pr[2], pr[3], __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), sl2, l4.z, l4.w);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) pr[f] = ex2_approx(pr[f]);
+          addmul2(ds[0], ds[1], __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), d4.x, d4.y, pr[0], pr[1]);
+          addmul2(ds[2], ds[3], __uint_as_float(pv[e + 2]), __uint_as_float(pv[e + 3]), d4.z, d4.w, pr[2], pr[3]);
+          if (!full) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int i = i0 + e + f;
+              if (key > i || (i - key >= p.window && key >= p.sink)) pr[f] = ds[f] = 0.f;
+            }
+          }
+          pp[e / 2] = pack_bf16x2(pr[0], pr[1]);
+          pp[e / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
+          dd[e / 2] = pack_bf16x2(ds[0], ds[1]);
+          dd[e / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
+        }
+        tmem_st32(tS, pp);
+        tmem_st32(tP, dd);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar.ds_full[grp]);
+      }
+      if (!ok) break;
+      ok = mbar_wait(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9);
+      if (!(ok = __all_sync(FULL, ok))) break;
+      ++an;
+      tc_fence_after();
+      // Group 0 writes dK, group 1 dV.
+      const bool isk = grp == 0;
+      const uint32_t ta = isk ? tK : tV;
+      const float scl = isk ? p.scale : 1.f;
+      if (w.part < 0) {
+        uint16_t *dst = isk ? p.dk + (int64_t)w.b * p.dk_sb + (int64_t)w.hk * p.dk_sh + (int64_t)key * p.dk_sn
+                            : p.dv + (int64_t)w.b * p.dv_sb + (int64_t)w.hk * p.dv_sh + (int64_t)key * p.dv_sn;
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(ta + c, o);
+          tmem_wait_ld();
+          if (key < p.N) store16(dst + c, o, scl);
+        }
+      } else {
+        float *dst = p.part + (((((int64_t)w.b * p.hkv + w.hk) * p.nst + w.kt) * (1 + p.nseg) + w.part) * 2 + grp) *
+                                  (kTileKeys * D) + r * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(ta + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bar.acc_empty[0]);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ join
+
+// dK, dV of the sinks' key tiles: part 0 (the band) and the far parts in order.  A block
+// per eight rows of one tile; 4 columns a thread.
+template <int D>
+__global__ void __launch_bounds__(256) swa_bwd_join_kernel(const SwaBwdParams p) {
+  const int tile = blockIdx.x;                       // (b, hk, kt)
+  const int kt = tile % p.nst, hk = tile / p.nst % p.hkv, b = tile / p.nst / p.hkv;
+  const int far = p.nt - 1 - swa_last_tile(kt, p.window, p.nt);
+  if (far <= 0) return;                              // written by the band's unit
+  const int parts = 1 + (p.G * far + p.seg - 1) / p.seg;
+  const int side = blockIdx.z;
+  for (int i = threadIdx.x; i < 8 * (D / 4); i += 256) {
+    const int r = blockIdx.y * 8 + i / (D / 4), c = (i % (D / 4)) * 4;
+    const int key = kt * kTileKeys + r;
+    if (key >= p.N) continue;
+    const float *src = p.part + ((int64_t)tile * (1 + p.nseg) * 2 + side) * (kTileKeys * D) + r * D + c;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < parts; ++x) {
+      const float4 y = *reinterpret_cast<const float4 *>(src + (int64_t)x * 2 * kTileKeys * D);
+      a[0] += y.x; a[1] += y.y; a[2] += y.z; a[3] += y.w;
+    }
+    const float s = side == 0 ? p.scale : 1.f;
+    uint16_t *dst = side == 0 ? p.dk + (int64_t)b * p.dk_sb + (int64_t)hk * p.dk_sh + (int64_t)key * p.dk_sn
+                              : p.dv + (int64_t)b * p.dv_sb + (int64_t)hk * p.dv_sh + (int64_t)key * p.dv_sn;
+    *reinterpret_cast<uint2 *>(dst + c) = make_uint2(pack_bf16x2(a[0] * s, a[1] * s), pack_bf16x2(a[2] * s, a[3] * s));
+  }
+}
+
+// ------------------------------------------------------------------ launch
+
+template <int D>
+static cudaError_t launch_swa_bwd_d(const CUtensorMap *m, const SwaBwdParams &p, int nsm, cudaStream_t st) {
+  const int groups = (p.nt * kTileRows + RowLanes<D>::RPW - 1) / RowLanes<D>::RPW;
+  long long blocks = ((long long)p.batch * p.hq * groups + 7) / 8;
+  if (blocks > (long long)nsm * 16) blocks = (long long)nsm * 16;
+  swa_bwd_prep_kernel<D><<<(unsigned)blocks, 256, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  e = cudaFuncSetAttribute(swa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaDqCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long items = (long long)p.batch * p.hq * p.nt;
+  swa_bwd_dq_kernel<D><<<(int)(items < nsm ? items : nsm), kSwaBwdThreads, SwaDqCfg<D>::SMEM, st>>>(
+      m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+  e = cudaFuncSetAttribute(swa_bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaDkvCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)p.batch * p.hkv * (p.nst * p.nseg + p.nt);
+  swa_bwd_dkdv_kernel<D><<<(int)(units < nsm ? units : nsm), kSwaBwdThreads, SwaDkvCfg<D>::SMEM, st>>>(
+      m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+  if (p.nst > 0) {
+    swa_bwd_join_kernel<D><<<dim3(p.batch * p.hkv * p.nst, kTileKeys / 8, 2), 256, 0, st>>>(p);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+// maps: Q, dO, K, V, each with its column tail (D != 64).
+cudaError_t launch_swa_bwd(const CUtensorMap *maps, const SwaBwdParams &p, int nsm, cudaStream_t st) {
+  switch (p.d) {
+    case 64: return launch_swa_bwd_d<64>(maps, p, nsm, st);
+    case 80: return launch_swa_bwd_d<80>(maps, p, nsm, st);
+    case 128: return launch_swa_bwd_d<128>(maps, p, nsm, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace moba

@@ -12,7 +12,11 @@
  *   moba_select_topk -> per-row block choices (idx) + block-major dispatch lists in
  *                       the workspace
  *   moba_attn_fwd    -> out and per-row log-sum-exp, reading the dispatch lists
- * swa_attn_fwd is independent (the window-only special case).
+ * swa_attn_fwd is independent (the window-only special case); swa_sink_attn_fwd keeps the
+ * first tokens visible too, and swa_attn_bwd is the backward of both.  Before the attention,
+ * qk_norm_rope_fwd normalises queries and keys per head and rotates them to their positions.
+ * A server appends new tokens to a paged cache with kv_append and attends one new token per
+ * sequence with paged_decode_attn.
  *
  * Conventions shared by every call:
  *   - Tensors are device pointers described by moba_tensor: element (b, h, n, 0) sits
@@ -37,7 +41,9 @@
  *   - Errors: calls return MOBA_OK (0) or a negative MOBA_ERR_* code.  Argument
  *     errors are detected on the host before anything is launched.  Kernel waits are
  *     bounded: a wait that runs out records MOBA_ERR_DEVICE in a device-side status
- *     word that moba_device_status() reads.
+ *     word that moba_device_status() reads.  Positions, lengths and page ids lie in device
+ *     memory, so the kernels check them: one out of range is never used as an address, and
+ *     records MOBA_ERR_INDEX in the same word.
  */
 #ifndef MOBA_H
 #define MOBA_H
@@ -59,6 +65,8 @@ extern "C" {
 #define MOBA_ERR_DEVICE -7    /* a kernel wait ran out (see moba_device_status) */
 #define MOBA_ERR_NODEVICE -8  /* no sm_100 device is current */
 #define MOBA_ERR_TOO_LARGE -9 /* problem needs more than moba_prefill_static's scratch */
+#define MOBA_ERR_INDEX -10    /* a position, length or page id in device memory is out of
+                                 range; what it names was left out (see moba_device_status) */
 
 typedef struct {
     void *ptr;
@@ -243,8 +251,138 @@ int moba_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, 
                   moba_tensor dv, void *bwd_workspace, size_t bwd_workspace_bytes, void *stream);
 
 /*
- * Reads and clears the device-side status word that bounded kernel waits write
- * (MOBA_OK or MOBA_ERR_DEVICE) on the current device.  Synchronises the device.
+ * Sliding-window attention whose first `sink` tokens stay visible (attention sinks at token
+ * granularity; moba_select_static has them at block granularity): swa_attn_fwd_chunk with
+ * M_ij = 0 iff j <= p_i and (p_i - j < window or j < sink), p_i = Nk - N + i.
+ *   sink : >= 0 (MOBA_ERR_ARG otherwise); 0 is swa_attn_fwd_chunk
+ * The other arguments and errors are swa_attn_fwd_chunk's.  k and v must be finite also at
+ * positions that a row does not see (they are multiplied by zero).
+ */
+int swa_sink_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, int hq, int hkv,
+                      int N, int Nk, int d, int window, int sink, float scale, moba_tensor out,
+                      float *lse, void *stream);
+
+/*
+ * Backward of swa_attn_fwd (sink = 0) and swa_sink_attn_fwd on whole sequences (Nk = N).
+ * With z_ij = scale q_i.k_j and p_ij = exp(z_ij - lse_i) over the keys that row i sees:
+ *     D_i = dO_i . o_i,  dz_ij = p_ij (dO_i . v_j - D_i),
+ *     dQ_i = scale sum_j dz_ij k_j,  dK_j = scale sum_i dz_ij q_i,  dV_j = sum_i p_ij dO_i
+ * (a KV head's dK and dV sum over the q-heads that read it).  d in {64, 80, 128}; any N.
+ *   q, k, v, out, lse : as given to / returned by the forward
+ *   dout       : bf16 upstream gradient [batch, hq, N, d]
+ *   dq         : bf16 out [batch, hq, N, d];  dk, dv : bf16 out [batch, hkv, N, d]
+ *   workspace  : device buffer of at least swa_bwd_workspace_size() bytes (row statistics,
+ *                and partial dK, dV of the sinks)
+ * No atomics: results are deterministic.
+ */
+int swa_bwd_workspace_size(int batch, int hq, int hkv, int N, int d, int window, int sink,
+                           size_t *bytes);
+int swa_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, moba_tensor dout,
+                 const float *lse, int batch, int hq, int hkv, int N, int d, int window, int sink,
+                 float scale, moba_tensor dq, moba_tensor dk, moba_tensor dv, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
+/*
+ * A weight of d values for the per-head norms: bf16 (f32 = 0, 2-byte aligned) or float32
+ * (f32 = 1, 4-byte aligned).  A null pointer: no norm.
+ */
+typedef struct {
+    const void *ptr;
+    int f32;
+} moba_weight;
+
+/*
+ * Norms of queries and keys per head and the position rotation in one pass, before the
+ * attention (which takes rotated q and k).  Row x of a head at position p becomes
+ *     xn = x / sqrt(mean(x^2) + eps) * weight        (xn = x without a weight)
+ * and the pairs (a, c) of its first `rot` columns become
+ *     (a cos - c sin, c cos + a sin)
+ * with the angles of position p; the columns from rot on are xn.  Pairs are the columns
+ * (i, i + rot / 2), or neighbours (2 i, 2 i + 1) when interleaved = 1.
+ *   q, k, q_out, k_out : bf16 [batch, hq|hkv, N, d], d in {64, 80, 128}; an output may be its
+ *                input itself
+ *   cosp, sinp : float32 [max_pos, rot / 2], contiguous, 16-byte aligned; rot a multiple of
+ *                16, 0 < rot <= d (MOBA_ERR_DIM otherwise)
+ *   positions  : int32 [batch, N] contiguous, or null: row n is at position n (then
+ *                max_pos >= N, MOBA_ERR_SHAPE otherwise).  A row whose position lies outside
+ *                [0, max_pos) is not written (MOBA_ERR_INDEX from moba_device_status).
+ *   eps        : >= 0
+ */
+int qk_norm_rope_fwd(moba_tensor q, moba_tensor k, const float *cosp, const float *sinp,
+                     const int32_t *positions, moba_weight q_weight, moba_weight k_weight, int batch,
+                     int hq, int hkv, int N, int d, int rot, int max_pos, int interleaved, float eps,
+                     moba_tensor q_out, moba_tensor k_out, void *stream);
+
+/*
+ * Backward of qk_norm_rope_fwd: with dy the gradient of a rotated row, g = R^T dy,
+ * r = 1 / sqrt(mean(x^2) + eps):
+ *     dx = r (g w - x r^2 mean(g w x)),  dw = sum over rows and heads of g x r
+ * (dx = g without a weight; q, k are then not read).
+ *   dq_out, dk_out : bf16 gradients of q_out, k_out;  q, k : the forward's inputs
+ *   dq, dk         : bf16 out; may be dq_out, dk_out themselves
+ *   dq_weight, dk_weight : float32 out [d] where the weight is not null (else null)
+ *   workspace      : device buffer of at least qk_norm_rope_bwd_workspace_size() bytes when
+ *                    there is a weight
+ * The rows' and arguments' rules are qk_norm_rope_fwd's.  No atomics: deterministic.
+ */
+int qk_norm_rope_bwd_workspace_size(int batch, int hq, int hkv, int N, int d, size_t *bytes);
+int qk_norm_rope_bwd(moba_tensor dq_out, moba_tensor dk_out, moba_tensor q, moba_tensor k,
+                     const float *cosp, const float *sinp, const int32_t *positions,
+                     moba_weight q_weight, moba_weight k_weight, int batch, int hq, int hkv, int N,
+                     int d, int rot, int max_pos, int interleaved, float eps, moba_tensor dq,
+                     moba_tensor dk, float *dq_weight, float *dk_weight, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Paged key-value cache: k_pages and v_pages are bf16 moba_tensors [num_pages, hkv, page, d]
+ * with strides sb (page), sh (KV head) and sn (slot), so that head-major and token-major
+ * pages are both views.  Position j of sequence b lies in slot j % page of page
+ * page_table[b, j / page] (int32 [batch, max_pages], contiguous).  page >= 1.
+ *
+ * kv_append writes the T new tokens of a batch into their sequences' pages.  Tokens
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [batch + 1]; null: T = batch, one token a
+ * sequence) belong to sequence b and take its last positions below seq_lens[b] (int32
+ * [batch], lengths with the new tokens).  Tokens behind cu_seqlens[batch] are left alone.
+ *   k, v       : bf16 [T, hkv, d]: sn between tokens, sh between heads (sb unused)
+ *   q, q_out   : bf16 [T, hq, d] likewise, or null pointers: queries normalised and rotated
+ *                to the same positions beside them
+ *   cosp, sinp, rot, max_pos, interleaved, eps, weights : as in qk_norm_rope_fwd, for k and q;
+ *                cosp = sinp = null: no rotation (rot 0)
+ * v is copied.  A token whose position is negative, outside the angle table or on a page
+ * that is not there ([0, num_pages)) writes nothing and records MOBA_ERR_INDEX.
+ */
+int kv_append(moba_tensor k, moba_tensor v, moba_tensor q, const int32_t *cu_seqlens,
+              const int32_t *seq_lens, const int32_t *page_table, const float *cosp,
+              const float *sinp, moba_weight q_weight, moba_weight k_weight, int batch, int T, int hq,
+              int hkv, int d, int rot, int max_pos, int interleaved, float eps, int page,
+              int num_pages, int max_pages, moba_tensor k_pages, moba_tensor v_pages,
+              moba_tensor q_out, void *stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache: the query of sequence b
+ * sits at position len - 1, len = seq_lens[b], and sees the keys j < len with
+ * window = 0, or len - 1 - j < window, or j < sink:
+ *     out_b = softmax(scale q_b K^T) V,  lse_b = log sum exp(scale q_b . k_j)
+ * A sequence that sees no key (len <= 0) gets out = 0 and lse = -inf.
+ *   q, out     : bf16 [batch, hq, d]: sb between sequences, sh between heads (sn unused)
+ *   lse        : float32 out [batch, hq], contiguous
+ *   workspace  : device buffer of at least paged_decode_workspace_size() bytes; it carries
+ *                nothing from call to call
+ * A length outside [0, max_pages * page] is taken as the nearest end, and keys on a page
+ * that is not there are left out; both record MOBA_ERR_INDEX.  Slots that no sequence sees
+ * are not read.  d in {64, 80, 128}; any hq / hkv.  No atomics: deterministic.
+ */
+int paged_decode_workspace_size(int batch, int hq, int hkv, int d, size_t *bytes);
+int paged_decode_attn(moba_tensor q, moba_tensor k_pages, moba_tensor v_pages,
+                      const int32_t *page_table, const int32_t *seq_lens, int batch, int hq, int hkv,
+                      int d, int page, int num_pages, int max_pages, int window, int sink,
+                      float scale, moba_tensor out, float *lse, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * Reads and clears the device-side status word that bounded kernel waits and index checks
+ * write (MOBA_OK, MOBA_ERR_DEVICE or MOBA_ERR_INDEX) on the current device.  Synchronises
+ * the device.
  */
 int moba_device_status(void);
 

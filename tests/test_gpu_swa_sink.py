@@ -1,0 +1,151 @@
+"""Sliding-window attention with sinks and its backward against the float64 formulas, value
+by value within what the roundings allow (tests/plain_ops.py derives the bounds)."""
+import pytest
+import torch
+
+from tests import plain_ops as po
+
+pytestmark = pytest.mark.gpu
+
+
+def _moba():
+    import block_sparse_long_prefill_b200 as moba
+    return moba
+
+
+def _inputs(batch, hq, hkv, n, nk, d, seed, strided=False):
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def rand(h, m):
+        if strided:  # token-major: the heads of a token lie side by side
+            return torch.randn(batch, m, h, d, generator=g, device="cuda").bfloat16().permute(0, 2, 1, 3)
+        return torch.randn(batch, h, m, d, generator=g, device="cuda").bfloat16()
+
+    return rand(hq, n), rand(hkv, nk), rand(hkv, nk), rand(hq, n)
+
+
+def _wide(x, G):
+    return x.double().repeat_interleave(G, 1)
+
+
+def _fwd(batch, hq, hkv, n, nk, d, window, sink, seed=0, strided=False, scale=0.0):
+    moba = _moba()
+    q, k, v, do = _inputs(batch, hq, hkv, n, nk, d, seed, strided)
+    out, lse = moba.swa_attn_fwd_chunk(q, k, v, window, scale, sink=sink)
+    assert moba.device_status() == 0
+    see = po.visible(n, nk, window, sink, "cuda")
+    G = hq // hkv
+    o, l, p, ob, lb = po.attention(q.double(), _wide(k, G), _wide(v, G), see, scale or None)
+    po.check("out", out, o, ob)
+    po.check("lse", lse, l, lb)
+    return (q, k, v, do), (out, lse), see, ob
+
+
+def _bwd(batch, hq, hkv, n, d, window, sink, seed=0, strided=False, scale=0.0):
+    moba = _moba()
+    (q, k, v, do), (out, lse), see, ob = _fwd(batch, hq, hkv, n, n, d, window, sink, seed, strided, scale)
+    dq, dk, dv = moba.swa_attn_bwd(q, k, v, out, lse, do, window, sink, scale)
+    assert moba.device_status() == 0
+    G = hq // hkv
+    (wq, bq), (wk, bk), (wv, bv) = po.attention_bwd(q.double(), _wide(k, G), _wide(v, G), do.double(), see,
+                                                    scale or None, ob)
+    fold = lambda x: x.view(batch, hkv, G, n, d).sum(2)  # noqa: E731
+    po.check("dq", dq, wq, bq)
+    # Stored after the sum over the heads: the heads' own bounds cover its rounding.
+    po.check("dk", dk, fold(wk), fold(bk))
+    po.check("dv", dv, fold(wv), fold(bv))
+    return (q, k, v, do, out, lse), (dq, dk, dv)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("n,window,sink", [(1, 1, 1), (5, 2, 1), (129, 1, 128), (257, 64, 4), (640, 128, 129),
+                                           (1000, 200, 4), (1000, 5000, 4), (777, 100, 2000), (1100, 130, 300)])
+def test_forward(d, n, window, sink):
+    _fwd(1, 2, 2, n, n, d, window, sink, seed=n)
+
+
+@pytest.mark.parametrize("d,hq,hkv,n,nk,window,sink", [
+    (64, 3, 1, 100, 1000, 77, 4), (80, 4, 2, 1, 1500, 300, 130), (128, 8, 2, 333, 900, 128, 1),
+    (128, 2, 2, 130, 131, 3, 2)])
+def test_forward_of_the_last_rows(d, hq, hkv, n, nk, window, sink):
+    _fwd(2, hq, hkv, n, nk, d, window, sink, seed=nk, strided=True)
+
+
+def test_forward_without_sinks_is_the_band():
+    moba = _moba()
+    q, k, v, _ = _inputs(1, 4, 2, 900, 900, 128, 3)
+    a, la = moba.swa_attn_fwd(q, k, v, 200)
+    b, lb = moba.swa_attn_fwd(q, k, v, 200, sink=0)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    # Sinks inside every row's window change nothing that is seen.
+    c, lc = moba.swa_attn_fwd(q[:, :, :150], k[:, :, :150], v[:, :, :150], 200, sink=9)
+    assert torch.equal(a[:, :, :150], c) and torch.equal(la[:, :, :150], lc)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("n,window,sink", [(1, 1, 0), (5, 2, 1), (128, 128, 0), (129, 1, 128), (257, 64, 4),
+                                           (640, 128, 129), (1000, 200, 4), (1000, 5000, 4), (900, 100, 2000)])
+def test_backward(d, n, window, sink):
+    _bwd(1, 2, 2, n, d, window, sink, seed=n)
+
+
+@pytest.mark.parametrize("d,batch,hq,hkv,n,window,sink", [
+    (64, 2, 6, 2, 500, 130, 5), (80, 2, 4, 1, 700, 60, 140), (128, 2, 8, 4, 520, 128, 130),
+    (128, 1, 3, 1, 3000, 1, 1), (64, 1, 8, 1, 3000, 100, 260), (80, 1, 1, 1, 2900, 250, 0)])
+def test_backward_of_shared_heads_and_split_sinks(d, batch, hq, hkv, n, window, sink):
+    _bwd(batch, hq, hkv, n, d, window, sink, seed=n, strided=True)
+
+
+def test_backward_with_a_scale_repeats_bit_for_bit():
+    moba = _moba()
+    (q, k, v, do, out, lse), grads = _bwd(1, 4, 2, 1500, 64, 90, 7, scale=0.3)
+    for _ in range(3):
+        again = moba.swa_attn_bwd(q, k, v, out, lse, do, 90, 7, 0.3)
+        assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_backward_equals_differences_of_the_forward():
+    """sum(dO out) along a direction, from the kernel's own forward in steps large enough to
+    stand above its bf16 rounding: out is off by at most 2^-8 of itself and of p |v| (a sum
+    of 2 n d such errors with random signs), the step is 1/4, so the quotient is good to a few
+    per cent of the gradient's norm along it."""
+    moba = _moba()
+    q, k, v, do = _inputs(1, 2, 1, 200, 200, 64, 5)
+    out, lse = moba.swa_attn_fwd(q, k, v, 50, sink=3)
+    dq, dk, dv = moba.swa_attn_bwd(q, k, v, out, lse, do, 50, sink=3)
+
+    def loss(v2):
+        o, _ = moba.swa_attn_fwd(q, k, v2, 50, sink=3)
+        return float((o.double() * do.double()).sum())
+
+    u = torch.randn(v.shape, generator=torch.Generator("cuda").manual_seed(6), device="cuda").bfloat16()
+    up, down = (v + 0.25 * u).bfloat16(), (v - 0.25 * u).bfloat16()
+    got, want = loss(up) - loss(down), float((dv.double() * (up.double() - down.double())).sum())
+    # (The loss is linear in v: no curvature.)  Each of the outputs, 2 x 200 x 64 of
+    # magnitude below 1 against dO of 1, carries up to 2^-7; the sum of their errors, of
+    # random sign, stays within six deviations of 2^-7 sqrt(2 x 25600).
+    assert abs(got - want) <= 6 * 2.0 ** -7 * (2 * 25600) ** 0.5, (got, want)
+
+
+def test_on_another_stream_and_in_a_graph():
+    moba = _moba()
+    q, k, v, do = _inputs(1, 4, 2, 700, 700, 80, 8)
+    out, lse = moba.swa_attn_fwd(q, k, v, 100, sink=5)
+    want = moba.swa_attn_bwd(q, k, v, out, lse, do, 100, 5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, l2 = moba.swa_attn_fwd(q, k, v, 100, sink=5, stream=side)
+    got = moba.swa_attn_bwd(q, k, v, o2, l2, do, 100, 5, stream=side)
+    side.synchronize()
+    assert torch.equal(out, o2) and all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o3, l3 = moba.swa_attn_fwd(q, k, v, 100, sink=5)
+        got = moba.swa_attn_bwd(q, k, v, o3, l3, do, 100, 5)
+    for _ in range(2):
+        for t in (o3, l3, *got):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, o3) and all(torch.equal(a, b) for a, b in zip(want, got))
+    assert moba.device_status() == 0
