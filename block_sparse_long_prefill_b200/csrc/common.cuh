@@ -103,6 +103,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
+// The wait of a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                               int *status, int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, site));
+}
+
 // -------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
@@ -169,6 +175,20 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ----------------------------------------------------------------- tcgen05
+
+// One lane of a converged warp, the same every time.  A warp that issues tcgen05.mma runs
+// its loop as a whole, waits included, and lets the elected lane issue: the instruction
+// takes its descriptors from uniform registers, and under a branch on the lane number the
+// compiler gathers each of them lane by lane.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
 
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem_slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(

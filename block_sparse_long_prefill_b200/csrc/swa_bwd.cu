@@ -255,7 +255,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char *sbase = smem_raw + (base - raw);
   SwaBars &bar = *reinterpret_cast<SwaBars *>(sbase + C::BAR_OFF);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int site0 = (40 * 16 + (D == 64 ? 0 : (D == 80 ? 1 : 2))) * 256;
   constexpr uint32_t FULL = 0xffffffffu;
   const int nitems = p.batch * p.hq * p.nt;
@@ -274,7 +274,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem_base;
+  const uint32_t tmem = __shfl_sync(FULL, bar.tmem_base, 0);   // (uniform)
   volatile int *abort = &bar.abort;
   // TMEM: S_x at 128 x, dP_x at 128 x + 64 (x: column half and group); dQ at 256 and 384.
 
@@ -313,37 +313,38 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      // Step by step over the chunks of all items: per half x, dQ += dS_x K_x of the last
-      // step (once group x has written dS over S_x), then S_x and dP_x of this step.
-      uint32_t step = 0, qn = 0, an = 0;   // steps, items begun, items whose dQ began
-      uint32_t sc[2] = {0u, 0u};
-      bool ok = true;
-      int u = blockIdx.x, m = 0;
-      SwaDqItem w{};
-      if (u < nitems) w = swa_dq_item(p, u);
-      bool prev = false, prev_first = false, prev_last = false;
-      while (ok && (u < nitems || prev)) {
-        const bool cur = u < nitems;
-        const uint32_t st = step % C::ST, pst = (step - 1) % C::ST;
-        const uint32_t qs = qn % C::QS;
-        if (cur) {
-          if (m == 0 && !(ok = mbar_wait(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
-          if (!(ok = mbar_wait(&bar.k_full[st], (step / C::ST) & 1, abort, p.status, site0 + 4))) break;
-          if (!(ok = mbar_wait(&bar.v_full[st], (step / C::ST) & 1, abort, p.status, site0 + 5))) break;
-          tc_fence_after();
-        }
+    // Step by step over the chunks of all items: per half x, dQ += dS_x K_x of the last
+    // step (once group x has written dS over S_x), then S_x and dP_x of this step.
+    uint32_t step = 0, qn = 0, an = 0;   // steps, items begun, items whose dQ began
+    uint32_t sc[2] = {0u, 0u};
+    bool ok = true;
+    int u = blockIdx.x, m = 0;
+    SwaDqItem w{};
+    if (u < nitems) w = swa_dq_item(p, u);
+    bool prev = false, prev_first = false, prev_last = false;
+    while (ok && (u < nitems || prev)) {
+      const bool cur = u < nitems;
+      const uint32_t st = step % C::ST, pst = (step - 1) % C::ST;
+      const uint32_t qs = qn % C::QS;
+      if (cur) {
+        if (m == 0 && !(ok = mbar_wait_warp(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
+        if (!(ok = mbar_wait_warp(&bar.k_full[st], (step / C::ST) & 1, abort, p.status, site0 + 4))) break;
+        if (!(ok = mbar_wait_warp(&bar.v_full[st], (step / C::ST) & 1, abort, p.status, site0 + 5))) break;
+      }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t tS = tmem + 128 * x, tP = tS + 64;
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t tS = tmem + 128 * x, tP = tS + 64;
+        if (prev) {
+          if (!(ok = mbar_wait_warp(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 6))) break;
+          ++sc[x];
+          if (x == 0 && prev_first) {
+            if (!(ok = mbar_wait_warp(&bar.acc_empty[an & 1], ((an >> 1) & 1) ^ 1, abort, p.status, site0 + 7))) break;
+            ++an;
+          }
+        }
+        tc_fence_after();
+        if (elect_one()) {
           if (prev) {
-            if (!(ok = mbar_wait(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 6))) break;
-            ++sc[x];
-            if (x == 0 && prev_first) {
-              if (!(ok = mbar_wait(&bar.acc_empty[an & 1], ((an >> 1) & 1) ^ 1, abort, p.status, site0 + 7))) break;
-              ++an;
-            }
-            tc_fence_after();
             const uint32_t kt = base + C::K_OFF + pst * T::TILE;
             const uint32_t tQ = tmem + 256 + 128 * ((an - 1) & 1);
 #pragma unroll
@@ -365,20 +366,23 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
           }
         }
-        if (!ok) break;
-        prev = cur;
-        if (cur) {
-          prev_first = m == 0;
-          prev_last = m == w.nc - 1;
-          ++step;
-          if (++m == w.nc) {
-            ++qn;
-            m = 0;
-            u += gridDim.x;
-            if (u < nitems) w = swa_dq_item(p, u);
-          }
+        __syncwarp();
+      }
+      if (!ok) break;
+      prev = cur;
+      if (cur) {
+        prev_first = m == 0;
+        prev_last = m == w.nc - 1;
+        ++step;
+        if (++m == w.nc) {
+          ++qn;
+          m = 0;
+          u += gridDim.x;
+          if (u < nitems) w = swa_dq_item(p, u);
         }
       }
+    }
+    if (elect_one()) {
       umma_commit(&bar.mma_done);
       const unsigned long long t0 = global_timer_ns();
       while (!mbar_try_wait(&bar.mma_done, 0) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
@@ -413,12 +417,16 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           float x0, x1, d0, d1;
           fma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, nl, nl);
           addmul2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), nd, nd, ex2_approx(x0), ex2_approx(x1));
-          if (!full) {
-            const int k0 = key0 + e, k1 = k0 + 1;
-            if (k0 > i || (i - k0 >= p.window && k0 >= p.sink)) d0 = 0.f;
-            if (k1 > i || (i - k1 >= p.window && k1 >= p.sink)) d1 = 0.f;
-          }
           ds[e / 2] = pack_bf16x2(d0, d1);
+        }
+        if (!full) {
+          // Keys that the row does not see: zero halves of the packed pairs.
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const int k0 = key0 + e, k1 = k0 + 1;
+            if (k0 > i || (i - k0 >= p.window && k0 >= p.sink)) ds[e / 2] &= 0xFFFF0000u;
+            if (k1 > i || (i - k1 >= p.window && k1 >= p.sink)) ds[e / 2] &= 0x0000FFFFu;
+          }
         }
         tmem_st32(tS, ds);
         tmem_wait_st();
@@ -529,7 +537,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char *sbase = smem_raw + (base - raw);
   SwaBars &bar = *reinterpret_cast<SwaBars *>(sbase + C::BAR_OFF);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int site0 = (41 * 16 + (D == 64 ? 0 : (D == 80 ? 1 : 2))) * 256;
   constexpr uint32_t FULL = 0xffffffffu;
   const int nunits = swa_dkv_units(p);
@@ -548,7 +556,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem_base;
+  const uint32_t tmem = __shfl_sync(FULL, bar.tmem_base, 0);   // (uniform)
   volatile int *abort = &bar.abort;
   // TMEM: S^T_x at 128 x, dP^T_x at 128 x + 64 (x: query half and group); dK at 256, dV at
   // 256 + D.
@@ -595,40 +603,41 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      // Step by step over the query tiles of all units: per half x, dV += P^T_x dO_x and
-      // dK += dS^T_x Q_x of the last step, then S^T_x and dP^T_x of this step.
-      uint32_t step = 0, kn = 0, an = 0;
-      uint32_t sc[2] = {0u, 0u};
-      bool ok = true;
-      SwaDkvUnit w{};
-      auto seek = [&](int v) {
-        while (v < nunits && !swa_dkv_unit(p, v, w)) v += gridDim.x;
-        return v;
-      };
-      int u = seek(blockIdx.x), t = w.t0;
-      bool prev = false, prev_first = false, prev_last = false;
-      const uint32_t tK = tmem + 256, tV = tmem + 256 + D;
-      while (ok && (u < nunits || prev)) {
-        const bool cur = u < nunits;
-        const uint32_t st = step % C::QS, pst = (step - 1) % C::QS, ks = kn % C::KS;
-        const bool last = t == w.t1 - 1;
-        if (cur) {
-          if (t == w.t0 && !(ok = mbar_wait(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3))) break;
-          if (!(ok = mbar_wait(&bar.q_full[st], (step / C::QS) & 1, abort, p.status, site0 + 4))) break;
-          tc_fence_after();
-        }
+    // Step by step over the query tiles of all units: per half x, dV += P^T_x dO_x and
+    // dK += dS^T_x Q_x of the last step, then S^T_x and dP^T_x of this step.
+    uint32_t step = 0, kn = 0, an = 0;
+    uint32_t sc[2] = {0u, 0u};
+    bool ok = true;
+    SwaDkvUnit w{};
+    auto seek = [&](int v) {
+      while (v < nunits && !swa_dkv_unit(p, v, w)) v += gridDim.x;
+      return v;
+    };
+    int u = seek(blockIdx.x), t = w.t0;
+    bool prev = false, prev_first = false, prev_last = false;
+    const uint32_t tK = tmem + 256, tV = tmem + 256 + D;
+    while (ok && (u < nunits || prev)) {
+      const bool cur = u < nunits;
+      const uint32_t st = step % C::QS, pst = (step - 1) % C::QS, ks = kn % C::KS;
+      const bool last = t == w.t1 - 1;
+      if (cur) {
+        if (t == w.t0 && !(ok = mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3))) break;
+        if (!(ok = mbar_wait_warp(&bar.q_full[st], (step / C::QS) & 1, abort, p.status, site0 + 4))) break;
+      }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t tS = tmem + 128 * x, tP = tS + 64;
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t tS = tmem + 128 * x, tP = tS + 64;
+        if (prev) {
+          if (!(ok = mbar_wait_warp(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 5))) break;
+          ++sc[x];
+          if (x == 0 && prev_first) {
+            if (!(ok = mbar_wait_warp(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 6))) break;
+            ++an;
+          }
+        }
+        tc_fence_after();
+        if (elect_one()) {
           if (prev) {
-            if (!(ok = mbar_wait(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 5))) break;
-            ++sc[x];
-            if (x == 0 && prev_first) {
-              if (!(ok = mbar_wait(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 6))) break;
-              ++an;
-            }
-            tc_fence_after();
             const uint32_t qp = base + C::Q_OFF + pst * T::TILE, gp = base + C::DO_OFF + pst * T::TILE;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -649,20 +658,23 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             if (x == 1 && last) umma_commit(&bar.k_empty[ks]);
           }
         }
-        if (!ok) break;
-        prev = cur;
-        if (cur) {
-          prev_first = t == w.t0;
-          prev_last = last;
-          ++step;
-          ++t;
-          if (last) {
-            ++kn;
-            u = seek(u + gridDim.x);
-            t = w.t0;
-          }
+        __syncwarp();
+      }
+      if (!ok) break;
+      prev = cur;
+      if (cur) {
+        prev_first = t == w.t0;
+        prev_last = last;
+        ++step;
+        ++t;
+        if (last) {
+          ++kn;
+          u = seek(u + gridDim.x);
+          t = w.t0;
         }
       }
+    }
+    if (elect_one()) {
       umma_commit(&bar.mma_done);
       const unsigned long long t0 = global_timer_ns();
       while (!mbar_try_wait(&bar.mma_done, 0) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
@@ -709,17 +721,21 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           for (int f = 0; f < 4; ++f) pr[f] = ex2_approx(pr[f]);
           addmul2(ds[0], ds[1], __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), d4.x, d4.y, pr[0], pr[1]);
           addmul2(ds[2], ds[3], __uint_as_float(pv[e + 2]), __uint_as_float(pv[e + 3]), d4.z, d4.w, pr[2], pr[3]);
-          if (!full) {
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const int i = i0 + e + f;
-              if (key > i || (i - key >= p.window && key >= p.sink)) pr[f] = ds[f] = 0.f;
-            }
-          }
           pp[e / 2] = pack_bf16x2(pr[0], pr[1]);
           pp[e / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
           dd[e / 2] = pack_bf16x2(ds[0], ds[1]);
           dd[e / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
+        }
+        if (!full) {
+          // Rows that do not see the key: zero halves of the packed pairs.
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const int ia = i0 + e, ib = ia + 1;
+            const uint32_t keep = ((key > ia || (ia - key >= p.window && key >= p.sink)) ? 0u : 0x0000FFFFu) |
+                                  ((key > ib || (ib - key >= p.window && key >= p.sink)) ? 0u : 0xFFFF0000u);
+            pp[e / 2] &= keep;
+            dd[e / 2] &= keep;
+          }
         }
         tmem_st32(tS, pp);
         tmem_st32(tP, dd);
