@@ -24,7 +24,7 @@
 // O += P V, so the exponentials and the MMAs overlap (the FA4 ping-pong).
 //   warp 0       TMA producers: lane 0 the query tiles (query-major) and K chunks of 128
 //                keys, lane 1 the V chunks (separate K and V rings)
-//   warp 1       tcgen05 MMA issuer (one thread) and TMEM owner
+//   warp 1       tcgen05 MMA issuer (an elected lane) and TMEM owner
 //   warps 2-3    query-row gather (gathered work): TMA gather4 of four rows per
 //                instruction, or cp.async when q's strides admit no 2-D row view
 //   warps 4-7    stream A softmax + epilogue; thread r owns row r (TMEM lane r)
@@ -297,7 +297,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char *sbase = smem_raw + (base - raw);
   Bars &bar = *reinterpret_cast<Bars *>(sbase + C::BAR_OFF);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int site0 = (MODE * 16 + (D == 64 ? 0 : (D == 80 ? 1 : 2))) * 256;
   constexpr uint32_t FULL = 0xffffffffu;
 
@@ -340,7 +340,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem_base;
+  const uint32_t tmem = __shfl_sync(FULL, bar.tmem_base, 0);   // (uniform)
   volatile int *abort = &bar.abort;
 
   // Register split (launch: 384 threads x 168): see kRegSplitTotal.
@@ -410,46 +410,48 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t idO64 = idesc_bf16(128, 64, 0, 1);
-        constexpr uint32_t idO128 = idesc_bf16(128, 128, 0, 1);
-        constexpr uint32_t idO16 = idesc_bf16(128, 16, 0, 1);
-        uint32_t kvc = 0;                      // pipeline slot of chunk 0 of this unit
-        uint32_t quse[2] = {0u, 0u}, pcnt[2] = {0u, 0u};
-        bool ok = true;
-        for (UnitIter<MODE> it(p, u_begin, u_end); ok && it.valid(); it.next()) {
-          Unit w;
-          it.get(p, w);
-          const bool act[2] = {w.t[0].rows > 0, w.t[1].rows > 0};
+      // The whole warp waits; its elected lane issues.
+      constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t idO64 = idesc_bf16(128, 64, 0, 1);
+      constexpr uint32_t idO128 = idesc_bf16(128, 128, 0, 1);
+      constexpr uint32_t idO16 = idesc_bf16(128, 16, 0, 1);
+      uint32_t kvc = 0;                      // pipeline slot of chunk 0 of this unit
+      uint32_t quse[2] = {0u, 0u}, pcnt[2] = {0u, 0u};
+      bool ok = true;
+      for (UnitIter<MODE> it(p, u_begin, u_end); ok && it.valid(); it.next()) {
+        Unit w;
+        it.get(p, w);
+        const bool act[2] = {w.t[0].rows > 0, w.t[1].rows > 0};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!act[x] || !ok) continue;
+          ok = mbar_wait_warp(&bar.q_full[x], quse[x] & 1, abort, p.status, site0 + 3);
+          ++quse[x];
+        }
+        if (!ok) break;
+        // Per chunk m, for each active stream: O += P V of chunk m-1, then S = Q K^T
+        // of chunk m (the stream's S buffer is free once its P was consumed).
+        for (int m = 0; m <= w.nc && ok; ++m) {
+          const uint32_t slot_m = kvc + m, slot_p = kvc + m - 1;
+          const int st_m = slot_m % C::ST, st_p = slot_p % C::ST;
+          if (m < w.nc) {
+            if (!(ok = mbar_wait_warp(&bar.k_full[st_m], (slot_m / C::ST) & 1, abort, p.status, site0 + 4))) break;
+          }
+          if (m > 0) {
+            if (!(ok = mbar_wait_warp(&bar.v_full[st_p], (slot_p / C::ST) & 1, abort, p.status, site0 + 6))) break;
+          }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!act[x] || !ok) continue;
-            ok = mbar_wait(&bar.q_full[x], quse[x] & 1, abort, p.status, site0 + 3);
-            ++quse[x];
-          }
-          if (!ok) break;
-          tc_fence_after();
-          // Per chunk m, for each active stream: O += P V of chunk m-1, then S = Q K^T
-          // of chunk m (the stream's S buffer is free once its P was consumed).
-          for (int m = 0; m <= w.nc && ok; ++m) {
-            const uint32_t slot_m = kvc + m, slot_p = kvc + m - 1;
-            const int st_m = slot_m % C::ST, st_p = slot_p % C::ST;
-            if (m < w.nc) {
-              if (!(ok = mbar_wait(&bar.k_full[st_m], (slot_m / C::ST) & 1, abort, p.status, site0 + 4))) break;
-            }
+            const uint32_t sb = tmem + 128 * x;
+            const uint32_t tO = tmem + 256 + 128 * x;
             if (m > 0) {
-              if (!(ok = mbar_wait(&bar.v_full[st_p], (slot_p / C::ST) & 1, abort, p.status, site0 + 6))) break;
+              if (!(ok = mbar_wait_warp(&bar.p_full[x], pcnt[x] & 1, abort, p.status, site0 + 5))) break;
+              ++pcnt[x];
             }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (!act[x] || !ok) continue;
-              const uint32_t sb = tmem + 128 * x;
-              const uint32_t tO = tmem + 256 + 128 * x;
+            tc_fence_after();
+            if (elect_one()) {
               if (m > 0) {
-                if (!(ok = mbar_wait(&bar.p_full[x], pcnt[x] & 1, abort, p.status, site0 + 5))) break;
-                ++pcnt[x];
-                tc_fence_after();
                 const uint32_t vt = base + C::V_OFF + st_p * C::TILE;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
@@ -474,13 +476,19 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (m == w.nc - 1) umma_commit(&bar.q_empty[x]);
               }
             }
-            if (!ok) break;
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (elect_one()) {
             if (m < w.nc) umma_commit(&bar.k_empty[st_m]);
             if (m > 0) umma_commit(&bar.v_empty[st_p]);
           }
-          kvc += w.nc;
+          __syncwarp();
         }
-        // Every MMA issued so far completes before TMEM is released.
+        kvc += w.nc;
+      }
+      // Every MMA issued so far completes before TMEM is released.
+      if (elect_one()) {
         umma_commit(&bar.mma_done);
         const unsigned long long t0 = global_timer_ns();
         while (!mbar_try_wait(&bar.mma_done, 0) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
