@@ -56,35 +56,38 @@ struct SwaTile {
   static_assert(BYTES == (uint32_t)TILE, "a tile is packed");
 };
 
-// K-major operand (rows = M or N), columns [16 ks, 16 ks + 16), from row 64 half on.
-template <int D>
-__device__ __forceinline__ uint64_t swa_kmajor(uint32_t tile, int ks, int half) {
-  if (ks < 4) return smem_desc(tile + half * 8192 + ks * 32, 16, 1024, kSwizzle128);
-  if (D == 128) return smem_desc(tile + SwaTile<D>::R0 + half * 8192 + (ks - 4) * 32, 16, 1024, kSwizzle128);
-  return smem_desc(tile + SwaTile<D>::R0 + half * 2048, 16, 256, kSwizzle32);
-}
+// High descriptor words: 128-byte swizzle (8-row groups 1024 bytes apart) and the 32-byte
+// swizzle of the D = 80 tail (256 bytes apart).
+constexpr uint32_t kHi128 = desc_hi(1024, kSwizzle128), kHi32 = desc_hi(256, kSwizzle32);
 
-// D[tmem, D columns] (+)= A[tmem, 16 columns of K] B[rows 16 kk .. of the tile, D columns].
+// D[tmem, D columns] (+)= A[tmem] B over the tile's rows [64 half, 64 half + 64): four steps
+// of 16 rows, A's in consecutive groups of 8 columns.  fresh: the first step overwrites.
 template <int D>
-__device__ __forceinline__ void swa_acc(uint32_t d, uint32_t a, uint32_t tile, int kk, uint32_t acc) {
-  if (D == 128) {
-    umma_ts(d, a, smem_desc(tile + kk * 2048, SwaTile<D>::R0, 1024, kSwizzle128),
-            idesc_bf16(128, 128, 0, 1), acc);
-  } else {
-    umma_ts(d, a, smem_desc(tile + kk * 2048, 16, 1024, kSwizzle128), idesc_bf16(128, 64, 0, 1), acc);
-    if (D == 80)
-      umma_ts(d + 64, a, smem_desc(tile + SwaTile<D>::R0 + kk * 512, 16, 256, kSwizzle32),
-              idesc_bf16(128, 16, 0, 1), acc);
+__device__ __forceinline__ void swa_acc(uint32_t d, uint32_t a, uint32_t tile, int half, bool fresh) {
+  const uint32_t b = desc_lo(tile, D == 128 ? SwaTile<D>::R0 : 16) + half * 512;
+  const uint32_t b1 = desc_lo(tile + SwaTile<D>::R0, 16) + half * 128;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    const uint32_t acc = (kk == 0 && fresh) ? 0u : 1u;
+    umma_ts_w(d, a + kk * 8, b + kk * 128, kHi128, idesc_bf16(128, D == 128 ? 128 : 64, 0, 1), acc);
+    if (D == 80) umma_ts_w(d + 64, a + kk * 8, b1 + kk * 32, kHi32, idesc_bf16(128, 16, 0, 1), acc);
   }
 }
 
-// S_half (64 columns) = A B_half^T over the D columns.
-template <int D>
-__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int half) {
-  constexpr uint32_t id = idesc_bf16(128, 64, 0, 0);
+// S (NB columns) = A B^T over the D columns; A and B K-major tiles, B's NB rows from row0 on.
+template <int D, int NB>
+__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int row0) {
+  constexpr uint32_t id = idesc_bf16(128, NB, 0, 0);
+  const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16) + row0 * 8;
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks)
-    umma_ss(d, swa_kmajor<D>(a, ks, 0), swa_kmajor<D>(b, ks, half), id, ks > 0 ? 1u : 0u);
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint32_t acc = ks > 0 ? 1u : 0u;
+    if (D == 80 && ks == 4)
+      umma_ss_w(d, al + SwaTile<D>::R0 / 16, kHi32, desc_lo(b + SwaTile<D>::R0, 16) + row0 * 2, kHi32, id, acc);
+    else
+      umma_ss_w(d, al + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128,
+                bl + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128, id, acc);
+  }
 }
 
 template <int D>
@@ -189,29 +192,39 @@ __device__ __forceinline__ int swa_dq_key(const SwaDqItem &w, int m) {
 template <int D>
 struct SwaDqCfg {
   static constexpr int QS = D == 128 ? 1 : 2;              // Q / dO stages
-  static constexpr int ST = D == 128 ? 2 : (D == 80 ? 3 : 4);  // K and V stages
+  static constexpr int NK = D == 128 ? 3 : (D == 80 ? 4 : 5);  // K stages (held until dQ)
+  static constexpr int NV = D == 128 ? 2 : (D == 80 ? 3 : 4);  // V stages
+  // TMEM: two S slots of 128 columns (dS is written back over them), dP, dQ.
+  static constexpr uint32_t P0 = 256, ACC = 384;
   static constexpr int Q_OFF = 0;
   static constexpr int DO_OFF = QS * SwaTile<D>::TILE;
   static constexpr int K_OFF = 2 * QS * SwaTile<D>::TILE;
-  static constexpr int V_OFF = K_OFF + ST * SwaTile<D>::TILE;
-  static constexpr int BAR_OFF = V_OFF + ST * SwaTile<D>::TILE;
+  static constexpr int V_OFF = K_OFF + NK * SwaTile<D>::TILE;
+  static constexpr int BAR_OFF = V_OFF + NV * SwaTile<D>::TILE;
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 struct SwaBars {
   uint64_t q_full[4], q_empty[4];
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], ds_full[2];      // per group: products ready; dS (and P) written back
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+  // Per group (dQ kernel: of both): products ready; read into registers; dS (and P) written
+  // back, of even and odd steps: a step's products are issued before the last step's
+  // write-back is waited for, so two write-backs may complete before that wait looks.
+  uint64_t s_full[2], p_empty[2], ds_full[2][2];
   uint64_t acc_full[2], acc_empty[2];  // accumulators final / read out
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
 };
 
-__device__ __forceinline__ void swa_init_bars(SwaBars &bar) {
+// warps: elementwise warps that arrive on the barriers of a step (each once).
+__device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps) {
   for (int s = 0; s < 4; ++s) {
     mbar_init(&bar.q_full[s], 1);
     mbar_init(&bar.q_empty[s], 1);
+  }
+  for (int s = 0; s < 5; ++s) {
     mbar_init(&bar.k_full[s], 1);
     mbar_init(&bar.k_empty[s], 1);
     mbar_init(&bar.v_full[s], 1);
@@ -219,9 +232,11 @@ __device__ __forceinline__ void swa_init_bars(SwaBars &bar) {
   }
   for (int x = 0; x < 2; ++x) {
     mbar_init(&bar.s_full[x], 1);
-    mbar_init(&bar.ds_full[x], 128);
+    mbar_init(&bar.p_empty[x], warps);
+    mbar_init(&bar.ds_full[x][0], warps);
+    mbar_init(&bar.ds_full[x][1], warps);
     mbar_init(&bar.acc_full[x], 1);
-    mbar_init(&bar.acc_empty[x], 256);
+    mbar_init(&bar.acc_empty[x], 8);
   }
   mbar_init(&bar.mma_done, 1);
   bar.abort = 0;
@@ -260,7 +275,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   constexpr uint32_t FULL = 0xffffffffu;
   const int nitems = p.batch * p.hq * p.nt;
 
-  if (tid == 0) swa_init_bars(bar);
+  if (tid == 0) swa_init_bars(bar, 8);
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmG);
@@ -276,7 +291,6 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(FULL, bar.tmem_base, 0);   // (uniform)
   volatile int *abort = &bar.abort;
-  // TMEM: S_x at 128 x, dP_x at 128 x + 64 (x: column half and group); dQ at 256 and 384.
 
   if (warp == 0) {
     if (lane < 2) {
@@ -286,18 +300,19 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       uint64_t *empty = kside ? bar.k_empty : bar.v_empty;
       const CUtensorMap *m0 = kside ? &tmK : &tmV, *m1 = kside ? &tmK1 : &tmV1;
       unsigned char *ring = sbase + (kside ? C::K_OFF : C::V_OFF);
+      const uint32_t stages = kside ? C::NK : C::NV;
       uint32_t cnt = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
         const SwaDqItem w = swa_dq_item(p, u);
         for (int m = 0; m < w.nc; ++m, ++cnt) {
-          const uint32_t st = cnt % C::ST;
-          if (!(ok = mbar_wait(&empty[st], ((cnt / C::ST) & 1) ^ 1, abort, p.status, site0 + 1))) break;
+          const uint32_t st = cnt % stages;
+          if (!(ok = mbar_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort, p.status, site0 + 1))) break;
           mbar_arrive_expect_tx(&full[st], T::BYTES);
           swa_load_tile<D>(ring + st * T::TILE, m0, m1, &full[st], swa_dq_key(w, m), w.hk, w.b);
         }
       }
-      if (*abort) drain_ring(full, cnt, C::ST, p.status);
+      if (*abort) drain_ring(full, cnt, stages, p.status);
     } else if (lane == 2) {
       // ---------------------------------------------------------- Q and dO
       uint32_t cnt = 0;
@@ -313,66 +328,47 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // Step by step over the chunks of all items: per half x, dQ += dS_x K_x of the last
-    // step (once group x has written dS over S_x), then S_x and dP_x of this step.
+    // Step by step over the chunks of all items: S and dP of this step as soon as the last
+    // step's have been read into registers, then dQ += dS K of the last step, once dS has been
+    // written back.  The next step's loads are waited for behind the products' issue, where
+    // the tensor core is busy.
     uint32_t step = 0, qn = 0, an = 0;   // steps, items begun, items whose dQ began
-    uint32_t sc[2] = {0u, 0u};
     bool ok = true;
     int u = blockIdx.x, m = 0;
     SwaDqItem w{};
-    if (u < nitems) w = swa_dq_item(p, u);
     bool prev = false, prev_first = false, prev_last = false;
+    auto loads = [&]() {                 // of step `step`, chunk m of item u
+      bool in = true;
+      if (m == 0) in = mbar_wait_warp(&bar.q_full[qn % C::QS], (qn / C::QS) & 1, abort, p.status, site0 + 3);
+      in = in && mbar_wait_warp(&bar.k_full[step % C::NK], (step / C::NK) & 1, abort, p.status, site0 + 4);
+      return in && mbar_wait_warp(&bar.v_full[step % C::NV], (step / C::NV) & 1, abort, p.status, site0 + 5);
+    };
+    if (u < nitems) {
+      w = swa_dq_item(p, u);
+      ok = loads();
+    }
     while (ok && (u < nitems || prev)) {
       const bool cur = u < nitems;
-      const uint32_t st = step % C::ST, pst = (step - 1) % C::ST;
-      const uint32_t qs = qn % C::QS;
+      const uint32_t pstep = step - 1;
       if (cur) {
-        if (m == 0 && !(ok = mbar_wait_warp(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
-        if (!(ok = mbar_wait_warp(&bar.k_full[st], (step / C::ST) & 1, abort, p.status, site0 + 4))) break;
-        if (!(ok = mbar_wait_warp(&bar.v_full[st], (step / C::ST) & 1, abort, p.status, site0 + 5))) break;
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t tS = tmem + 128 * x, tP = tS + 64;
-        if (prev) {
-          if (!(ok = mbar_wait_warp(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 6))) break;
-          ++sc[x];
-          if (x == 0 && prev_first) {
-            if (!(ok = mbar_wait_warp(&bar.acc_empty[an & 1], ((an >> 1) & 1) ^ 1, abort, p.status, site0 + 7))) break;
-            ++an;
-          }
-        }
+        if (!(ok = mbar_wait_warp(&bar.p_empty[0], (step & 1) ^ 1, abort, p.status, site0 + 10))) break;
         tc_fence_after();
         if (elect_one()) {
-          if (prev) {
-            const uint32_t kt = base + C::K_OFF + pst * T::TILE;
-            const uint32_t tQ = tmem + 256 + 128 * ((an - 1) & 1);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              swa_acc<D>(tQ, tS + kk * 8, kt, 4 * x + kk, (prev_first && x == 0 && kk == 0) ? 0u : 1u);
-            if (x == 1) {
-              umma_commit(&bar.k_empty[pst]);
-              if (prev_last) umma_commit(&bar.acc_full[(an - 1) & 1]);
-            }
-          }
-          if (cur) {
-            const uint32_t qt = base + C::Q_OFF + qs * T::TILE, gt = base + C::DO_OFF + qs * T::TILE;
-            swa_scores<D>(tS, qt, base + C::K_OFF + st * T::TILE, x);
-            swa_scores<D>(tP, gt, base + C::V_OFF + st * T::TILE, x);
-            umma_commit(&bar.s_full[x]);
-            if (x == 1) {
-              umma_commit(&bar.v_empty[st]);
-              if (m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
-            }
-          }
+          const uint32_t qs = qn % C::QS, vst = step % C::NV;
+          swa_scores<D, 128>(tmem + 128 * (step & 1), base + C::Q_OFF + qs * T::TILE,
+                             base + C::K_OFF + (step % C::NK) * T::TILE, 0);
+          swa_scores<D, 128>(tmem + C::P0, base + C::DO_OFF + qs * T::TILE, base + C::V_OFF + vst * T::TILE, 0);
+          umma_commit(&bar.s_full[0]);
+          umma_commit(&bar.v_empty[vst]);
+          if (m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
         }
         __syncwarp();
       }
-      if (!ok) break;
+      const bool pf = prev_first, pl = prev_last, had = prev;
       prev = cur;
+      prev_first = m == 0;
+      prev_last = m == w.nc - 1;
       if (cur) {
-        prev_first = m == 0;
-        prev_last = m == w.nc - 1;
         ++step;
         if (++m == w.nc) {
           ++qn;
@@ -380,6 +376,23 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           u += gridDim.x;
           if (u < nitems) w = swa_dq_item(p, u);
         }
+        if (u < nitems && !(ok = loads())) break;
+      }
+      if (had) {
+        if (!(ok = mbar_wait_warp(&bar.ds_full[0][pstep & 1], (pstep >> 1) & 1, abort, p.status, site0 + 6))) break;
+        if (pf) {
+          if (!(ok = mbar_wait_warp(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 7))) break;
+          ++an;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t kt = base + C::K_OFF + (pstep % C::NK) * T::TILE, tS = tmem + 128 * (pstep & 1);
+          swa_acc<D>(tmem + C::ACC, tS, kt, 0, pf);
+          swa_acc<D>(tmem + C::ACC, tS + 64, kt, 1, false);
+          umma_commit(&bar.k_empty[pstep % C::NK]);
+          if (pl) umma_commit(&bar.acc_full[0]);
+        }
+        __syncwarp();
       }
     }
     if (elect_one()) {
@@ -389,70 +402,93 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
   } else {
     // ------------------------------------------------------------ dS, and dQ out
+    // Group grp takes the columns [64 grp, 64 grp + 64) of S and dP.  An item's dQ is read
+    // out behind the first chunk of the next item, when its last product is long done.
     const int q4 = warp & 3, grp = (warp - 2) >> 2;
     const int r = 32 * q4 + lane;                   // row == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    const uint32_t tS = tmem + lane_off + 128 * grp, tP = tS + 64;
+    const uint32_t tP = tmem + lane_off + C::P0 + 64 * grp;
     const float sl2 = p.scale_log2;
     uint32_t sc = 0, an = 0;
     bool ok = true;
+    uint16_t *dst = nullptr;                        // the last item's row of dQ
+    bool live = false, pend = false;
+    auto read_out = [&]() {
+      bool in = mbar_wait(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9);
+      if (!__all_sync(FULL, in)) return false;
+      ++an;
+      tc_fence_after();
+      // A lane's 16 columns are one whole 32-byte sector of its row.
+      constexpr int CUT = D == 80 ? 48 : D / 2;     // columns of group 0
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        if ((c < CUT) != (grp == 0)) continue;
+        uint32_t o[16];
+        tmem_ld16(tmem + lane_off + C::ACC + c, o);
+        tmem_wait_ld();
+        if (live) store16(dst + c, o, p.scale);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.acc_empty[0]);
+      return true;
+    };
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
       const SwaDqItem w = swa_dq_item(p, u);
       const int i0 = w.qt * kTileRows, i = i0 + r;
       const float *st = p.stat + (((int64_t)w.b * p.hq + w.h) * p.nt + w.qt) * 256 + r;
       const float nl = st[0], nd = st[128];
       for (int m = 0; m < w.nc; ++m, ++sc) {
-        ok = mbar_wait(&bar.s_full[grp], sc & 1, abort, p.status, site0 + 8);
+        ok = mbar_wait(&bar.s_full[0], sc & 1, abort, p.status, site0 + 8);
         if (!(ok = __all_sync(FULL, ok))) break;
         tc_fence_after();
         const int key0 = swa_dq_key(w, m) + 64 * grp;
         const bool full = key0 + 63 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 64 <= p.sink);
+        const uint32_t tS = tmem + lane_off + 128 * (sc & 1) + 64 * grp;
         uint32_t sv[64], pv[64];
         tmem_ld64(tS, sv);
         tmem_ld64(tP, pv);
         tmem_wait_ld();
-        uint32_t ds[32];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_empty[0]);
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float x0, x1, d0, d1;
-          fma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, nl, nl);
-          addmul2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), nd, nd, ex2_approx(x0), ex2_approx(x1));
-          ds[e / 2] = pack_bf16x2(d0, d1);
-        }
-        if (!full) {
-          // Keys that the row does not see: zero halves of the packed pairs.
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t ds[16];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            const int k0 = key0 + e, k1 = k0 + 1;
-            if (k0 > i || (i - k0 >= p.window && k0 >= p.sink)) ds[e / 2] &= 0xFFFF0000u;
-            if (k1 > i || (i - k1 >= p.window && k1 >= p.sink)) ds[e / 2] &= 0x0000FFFFu;
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1, d0, d1;
+            fma2(x0, x1, __uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1]), sl2, nl, nl);
+            addmul2(d0, d1, __uint_as_float(pv[c + e]), __uint_as_float(pv[c + e + 1]), nd, nd, ex2_approx(x0),
+                    ex2_approx(x1));
+            ds[e / 2] = pack_bf16x2(d0, d1);
           }
+          if (!full) {
+            // Keys that the row does not see: zero halves of the packed pairs.
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const int k0 = key0 + c + e, k1 = k0 + 1;
+              if (k0 > i || (i - k0 >= p.window && k0 >= p.sink)) ds[e / 2] &= 0xFFFF0000u;
+              if (k1 > i || (i - k1 >= p.window && k1 >= p.sink)) ds[e / 2] &= 0x0000FFFFu;
+            }
+          }
+          tmem_st16(tS + c / 2, ds);
         }
-        tmem_st32(tS, ds);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar.ds_full[grp]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ds_full[0][sc & 1]);
+        if (pend) {
+          pend = false;
+          if (!(ok = read_out())) break;
+        }
       }
       if (!ok) break;
-      ok = mbar_wait(&bar.acc_full[an & 1], (an >> 1) & 1, abort, p.status, site0 + 9);
-      if (!(ok = __all_sync(FULL, ok))) break;
-      tc_fence_after();
-      // A lane's 16 columns are one whole 32-byte sector of its row.
-      uint16_t *dst = p.dq + (int64_t)w.b * p.dq_sb + (int64_t)w.h * p.dq_sh + (int64_t)i * p.dq_sn;
-      constexpr int CUT = D == 80 ? 48 : D / 2;     // columns of group 0
-      const uint32_t tQ = tmem + lane_off + 256 + 128 * (an & 1);
-      ++an;
-#pragma unroll
-      for (int c = 0; c < D; c += 16) {
-        if ((c < CUT) != (grp == 0)) continue;
-        uint32_t o[16];
-        tmem_ld16(tQ + c, o);
-        tmem_wait_ld();
-        if (i < p.N) store16(dst + c, o, p.scale);
-      }
-      tc_fence_before();
-      mbar_arrive(&bar.acc_empty[(an - 1) & 1]);
+      dst = p.dq + (int64_t)w.b * p.dq_sb + (int64_t)w.h * p.dq_sh + (int64_t)i * p.dq_sn;
+      live = i < p.N;
+      pend = true;
     }
+    if (ok && pend) read_out();
   }
 
   __syncwarp();
@@ -510,6 +546,18 @@ __device__ __forceinline__ bool swa_dkv_unit(const SwaBwdParams &p, int u, SwaDk
   return w.t0 < w.t1;
 }
 
+// TMEM of the dK / dV kernel: the halves' S in a ring of `S` slots of 64 columns (P and dS
+// are written back over them), their dP in a ring of two, then the accumulators.  With
+// three S slots a half's products are issued as soon as the half before the last has been
+// read into registers, while its group still computes; dK and dV of 128 columns leave room
+// for two, and a half's products wait for its group's write-back.
+template <int SLOTS>
+struct SwaTmem {
+  static constexpr int S = SLOTS;
+  static constexpr uint32_t P0 = 64 * S, ACC = P0 + 128;
+  static __device__ __forceinline__ uint32_t s_at(uint32_t h) { return 64 * (h % S); }
+};
+
 template <int D>
 struct SwaDkvCfg {
   static constexpr int KS = D == 128 ? 1 : 2;                  // K / V stages
@@ -521,6 +569,9 @@ struct SwaDkvCfg {
   static constexpr int ST_OFF = DO_OFF + QS * SwaTile<D>::TILE;
   static constexpr int BAR_OFF = ST_OFF + QS * 1024;
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  using M = SwaTmem<D == 128 ? 2 : 3>;
+  static_assert(M::ACC + 2 * D <= 512, "TMEM columns");
 };
 
 template <int D>
@@ -542,7 +593,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   constexpr uint32_t FULL = 0xffffffffu;
   const int nunits = swa_dkv_units(p);
 
-  if (tid == 0) swa_init_bars(bar);
+  if (tid == 0) swa_init_bars(bar, 4);
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmG);
@@ -558,8 +609,6 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(FULL, bar.tmem_base, 0);   // (uniform)
   volatile int *abort = &bar.abort;
-  // TMEM: S^T_x at 128 x, dP^T_x at 128 x + 64 (x: query half and group); dK at 256, dV at
-  // 256 + D.
 
   if (warp == 0) {
     if (lane == 0) {
@@ -603,10 +652,11 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // Step by step over the query tiles of all units: per half x, dV += P^T_x dO_x and
-    // dK += dS^T_x Q_x of the last step, then S^T_x and dP^T_x of this step.
+    // Step by step over the query tiles of all units, per half x: S^T_x and dP^T_x of this
+    // step, and dV += P^T_x dO_x, dK += dS^T_x Q_x of the last step; with two S slots the
+    // last step's come first, since they free the slot.
+    using M = typename C::M;
     uint32_t step = 0, kn = 0, an = 0;
-    uint32_t sc[2] = {0u, 0u};
     bool ok = true;
     SwaDkvUnit w{};
     auto seek = [&](int v) {
@@ -615,7 +665,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     };
     int u = seek(blockIdx.x), t = w.t0;
     bool prev = false, prev_first = false, prev_last = false;
-    const uint32_t tK = tmem + 256, tV = tmem + 256 + D;
+    const uint32_t tK = tmem + M::ACC, tV = tK + D;
     while (ok && (u < nunits || prev)) {
       const bool cur = u < nunits;
       const uint32_t st = step % C::QS, pst = (step - 1) % C::QS, ks = kn % C::KS;
@@ -625,40 +675,41 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         if (!(ok = mbar_wait_warp(&bar.q_full[st], (step / C::QS) & 1, abort, p.status, site0 + 4))) break;
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t tS = tmem + 128 * x, tP = tS + 64;
-        if (prev) {
-          if (!(ok = mbar_wait_warp(&bar.ds_full[x], sc[x] & 1, abort, p.status, site0 + 5))) break;
-          ++sc[x];
+      for (int y = 0; y < 4; ++y) {
+        const int x = y >> 1;
+        const uint32_t h = 2 * step + x;
+        if (((y & 1) == 0) == (M::S == 3)) {
+          if (!cur) continue;
+          if (!(ok = mbar_wait_warp(&bar.p_empty[x], (step & 1) ^ 1, abort, p.status, site0 + 10))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
+            swa_scores<D, 64>(tmem + M::s_at(h), kt, base + C::Q_OFF + st * T::TILE, 64 * x);
+            swa_scores<D, 64>(tmem + M::P0 + 64 * x, vt, base + C::DO_OFF + st * T::TILE, 64 * x);
+            umma_commit(&bar.s_full[x]);
+            if (x == 1 && last) umma_commit(&bar.k_empty[ks]);
+          }
+          __syncwarp();
+        } else {
+          if (!prev) continue;
+          if (!(ok = mbar_wait_warp(&bar.ds_full[x][(step - 1) & 1], ((step - 1) >> 1) & 1, abort, p.status, site0 + 5))) break;
           if (x == 0 && prev_first) {
             if (!(ok = mbar_wait_warp(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 6))) break;
             ++an;
           }
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          if (prev) {
+          tc_fence_after();
+          if (elect_one()) {
             const uint32_t qp = base + C::Q_OFF + pst * T::TILE, gp = base + C::DO_OFF + pst * T::TILE;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t acc = (prev_first && x == 0 && kk == 0) ? 0u : 1u;
-              swa_acc<D>(tV, tS + kk * 8, gp, 4 * x + kk, acc);
-              swa_acc<D>(tK, tP + kk * 8, qp, 4 * x + kk, acc);
-            }
+            const uint32_t tS = tmem + M::s_at(h - 2);   // P^T, then dS^T
+            swa_acc<D>(tV, tS, gp, x, prev_first && x == 0);
+            swa_acc<D>(tK, tS + 32, qp, x, prev_first && x == 0);
             if (x == 1) {
               umma_commit(&bar.q_empty[pst]);
               if (prev_last) umma_commit(&bar.acc_full[0]);
             }
           }
-          if (cur) {
-            const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
-            swa_scores<D>(tS, kt, base + C::Q_OFF + st * T::TILE, x);
-            swa_scores<D>(tP, vt, base + C::DO_OFF + st * T::TILE, x);
-            umma_commit(&bar.s_full[x]);
-            if (x == 1 && last) umma_commit(&bar.k_empty[ks]);
-          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (!ok) break;
       prev = cur;
@@ -672,6 +723,8 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           u = seek(u + gridDim.x);
           t = w.t0;
         }
+      } else {
+        break;
       }
     }
     if (elect_one()) {
@@ -684,8 +737,9 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int q4 = warp & 3, grp = (warp - 2) >> 2;
     const int r = 32 * q4 + lane;                   // key of the tile == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    const uint32_t tS = tmem + lane_off + 128 * grp, tP = tS + 64;
-    const uint32_t tK = tmem + lane_off + 256, tV = tK + D;
+    using M = typename C::M;
+    const uint32_t tP = tmem + lane_off + M::P0 + 64 * grp;
+    const uint32_t tK = tmem + lane_off + M::ACC, tV = tK + D;
     const float sl2 = p.scale_log2;
     uint32_t sc = 0, an = 0;
     bool ok = true;
@@ -705,43 +759,52 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const int i0 = qt * kTileRows + 64 * grp;   // row of the group's first column
         const bool full = key0 + kTileKeys - 1 <= i0 && (i0 + 63 - key0 < p.window || key0 + kTileKeys <= p.sink);
         if (++qt == w.first + w.len) qt = w.first;
+        const uint32_t tS = tmem + lane_off + M::s_at(2 * sc + grp);
         uint32_t sv[64], pv[64];
         tmem_ld64(tS, sv);
         tmem_ld64(tP, pv);
         tmem_wait_ld();
-        uint32_t pp[32], dd[32];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_empty[grp]);
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          const float4 l4 = *reinterpret_cast<const float4 *>(nl + e);
-          const float4 d4 = *reinterpret_cast<const float4 *>(nl + 128 + e);
-          float pr[4], ds[4];
-          fma2(pr[0], pr[1], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, l4.x, l4.y);
-          fma2(pr[2], pr[3], __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), sl2, l4.z, l4.w);
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t pp[16], dd[16];
 #pragma unroll
-          for (int f = 0; f < 4; ++f) pr[f] = ex2_approx(pr[f]);
-          addmul2(ds[0], ds[1], __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), d4.x, d4.y, pr[0], pr[1]);
-          addmul2(ds[2], ds[3], __uint_as_float(pv[e + 2]), __uint_as_float(pv[e + 3]), d4.z, d4.w, pr[2], pr[3]);
-          pp[e / 2] = pack_bf16x2(pr[0], pr[1]);
-          pp[e / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
-          dd[e / 2] = pack_bf16x2(ds[0], ds[1]);
-          dd[e / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
-        }
-        if (!full) {
-          // Rows that do not see the key: zero halves of the packed pairs.
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l4 = *reinterpret_cast<const float4 *>(nl + c + e);
+            const float4 d4 = *reinterpret_cast<const float4 *>(nl + 128 + c + e);
+            const float *sf = reinterpret_cast<const float *>(sv + c + e), *pf = reinterpret_cast<const float *>(pv + c + e);
+            float pr[4], ds[4];
+            fma2(pr[0], pr[1], sf[0], sf[1], sl2, l4.x, l4.y);
+            fma2(pr[2], pr[3], sf[2], sf[3], sl2, l4.z, l4.w);
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            const int ia = i0 + e, ib = ia + 1;
-            const uint32_t keep = ((key > ia || (ia - key >= p.window && key >= p.sink)) ? 0u : 0x0000FFFFu) |
-                                  ((key > ib || (ib - key >= p.window && key >= p.sink)) ? 0u : 0xFFFF0000u);
-            pp[e / 2] &= keep;
-            dd[e / 2] &= keep;
+            for (int f = 0; f < 4; ++f) pr[f] = ex2_approx(pr[f]);
+            addmul2(ds[0], ds[1], pf[0], pf[1], d4.x, d4.y, pr[0], pr[1]);
+            addmul2(ds[2], ds[3], pf[2], pf[3], d4.z, d4.w, pr[2], pr[3]);
+            pp[e / 2] = pack_bf16x2(pr[0], pr[1]);
+            pp[e / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
+            dd[e / 2] = pack_bf16x2(ds[0], ds[1]);
+            dd[e / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
           }
+          if (!full) {
+            // Rows that do not see the key: zero halves of the packed pairs.
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const int ia = i0 + c + e, ib = ia + 1;
+              const uint32_t keep = ((key > ia || (ia - key >= p.window && key >= p.sink)) ? 0u : 0x0000FFFFu) |
+                                    ((key > ib || (ib - key >= p.window && key >= p.sink)) ? 0u : 0xFFFF0000u);
+              pp[e / 2] &= keep;
+              dd[e / 2] &= keep;
+            }
+          }
+          tmem_st16(tS + c / 2, pp);
+          tmem_st16(tS + 32 + c / 2, dd);
         }
-        tmem_st32(tS, pp);
-        tmem_st32(tP, dd);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar.ds_full[grp]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ds_full[grp][sc & 1]);
       }
       if (!ok) break;
       ok = mbar_wait(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9);
@@ -776,7 +839,8 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         }
       }
       tc_fence_before();
-      mbar_arrive(&bar.acc_empty[0]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.acc_empty[0]);
     }
   }
 
