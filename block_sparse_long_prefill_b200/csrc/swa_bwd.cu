@@ -28,9 +28,15 @@
 // elementwise work goes in two groups of four warps, each with its half of the columns and
 // its own TMEM buffers, and the steps of consecutive items run on without a gap: the next
 // item's first products are issued before the last item's are summed up.
-//   warp 0      TMA: K, V, and Q with dO (and their row statistics) in rings of their own
-//   warp 1      tcgen05 issuer (one thread) and TMEM owner
-//   warps 2-9   elementwise groups 0 and 1; a thread owns one TMEM lane
+//   warp 0      TMA: K and V
+//   warp 1      issues S and dP (TMEM owner)
+//   warp 2      issues the accumulating products
+//   warp 3      TMA: Q with dO (and the row statistics)
+//   warps 4-11  elementwise groups 0 and 1; a thread owns one TMEM lane
+// Issue blocks until the tensor core has room, and a wait costs 85 cycles even when its
+// phase is complete, so one warp that issues everything leaves the tensor core idle during
+// its waits; two overlap theirs.  Every role runs as a whole warp: a lane that polls alone
+// under divergence sees a phase 400-700 cycles late, a whole warp 130.
 // Every wait is bounded, as in the forward.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,7 +49,7 @@
 
 namespace moba {
 
-constexpr int kSwaBwdThreads = 320;
+constexpr int kSwaBwdThreads = 384;
 
 // A 128-row tile of D columns: a 64-column region with 128-byte swizzle, then columns
 // [64, 128) the same way (D = 128) or [64, 80) with 32-byte swizzle (D = 80).
@@ -212,8 +218,9 @@ struct SwaBars {
   // back, of even and odd steps: a step's products are issued before the last step's
   // write-back is waited for, so two write-backs may complete before that wait looks.
   uint64_t s_full[2], p_empty[2], ds_full[2][2];
+  uint64_t slot_empty[3];              // the S slot's write-back consumed
   uint64_t acc_full[2], acc_empty[2];  // accumulators final / read out
-  uint64_t mma_done;
+  uint64_t mma_done[2];                // per issuing warp
   uint32_t tmem_base;
   int abort;
 };
@@ -238,9 +245,21 @@ __device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps) {
     mbar_init(&bar.acc_full[x], 1);
     mbar_init(&bar.acc_empty[x], 8);
   }
-  mbar_init(&bar.mma_done, 1);
+  for (int x = 0; x < 3; ++x) mbar_init(&bar.slot_empty[x], 1);
+  mbar_init(&bar.mma_done[0], 1);
+  mbar_init(&bar.mma_done[1], 1);
   bar.abort = 0;
   fence_barrier_init();
+}
+
+// The end of an issuing warp: everything it issued completes (within the wait limit)
+// before TMEM is released.
+__device__ __forceinline__ void swa_issued(uint64_t *done, const int *status) {
+  if (elect_one()) {
+    umma_commit(done);
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(done, 0) && global_timer_ns() - t0 < wait_limit_ns(status)) {}
+  }
 }
 
 // 16 columns of accumulators, scaled, as bf16 to a row.
@@ -293,118 +312,105 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   volatile int *abort = &bar.abort;
 
   if (warp == 0) {
-    if (lane < 2) {
-      // ---------------------------------------------------------- K (lane 0), V (lane 1)
-      const bool kside = lane == 0;
-      uint64_t *full = kside ? bar.k_full : bar.v_full;
-      uint64_t *empty = kside ? bar.k_empty : bar.v_empty;
-      const CUtensorMap *m0 = kside ? &tmK : &tmV, *m1 = kside ? &tmK1 : &tmV1;
-      unsigned char *ring = sbase + (kside ? C::K_OFF : C::V_OFF);
-      const uint32_t stages = kside ? C::NK : C::NV;
-      uint32_t cnt = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
-        const SwaDqItem w = swa_dq_item(p, u);
-        for (int m = 0; m < w.nc; ++m, ++cnt) {
-          const uint32_t st = cnt % stages;
-          if (!(ok = mbar_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort, p.status, site0 + 1))) break;
-          mbar_arrive_expect_tx(&full[st], T::BYTES);
-          swa_load_tile<D>(ring + st * T::TILE, m0, m1, &full[st], swa_dq_key(w, m), w.hk, w.b);
+    // ------------------------------------------------------------ V and K
+    uint32_t cnt = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
+      const SwaDqItem w = swa_dq_item(p, u);
+      for (int m = 0; m < w.nc; ++m, ++cnt) {
+        const uint32_t vs = cnt % C::NV, ks = cnt % C::NK;
+        if (!(ok = mbar_wait_warp(&bar.v_empty[vs], ((cnt / C::NV) & 1) ^ 1, abort, p.status, site0 + 1))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar.v_full[vs], T::BYTES);
+          swa_load_tile<D>(sbase + C::V_OFF + vs * T::TILE, &tmV, &tmV1, &bar.v_full[vs], swa_dq_key(w, m), w.hk, w.b);
         }
+        __syncwarp();
+        if (!(ok = mbar_wait_warp(&bar.k_empty[ks], ((cnt / C::NK) & 1) ^ 1, abort, p.status, site0 + 1))) {
+          ++cnt;       // (V was issued)
+          break;
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar.k_full[ks], T::BYTES);
+          swa_load_tile<D>(sbase + C::K_OFF + ks * T::TILE, &tmK, &tmK1, &bar.k_full[ks], swa_dq_key(w, m), w.hk, w.b);
+        }
+        __syncwarp();
       }
-      if (*abort) drain_ring(full, cnt, stages, p.status);
-    } else if (lane == 2) {
-      // ---------------------------------------------------------- Q and dO
-      uint32_t cnt = 0;
-      for (int u = blockIdx.x; u < nitems; u += gridDim.x, ++cnt) {
-        const SwaDqItem w = swa_dq_item(p, u);
-        const uint32_t st = cnt % C::QS;
-        if (!mbar_wait(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2)) break;
+    }
+    if (*abort) {
+      drain_ring(bar.v_full, cnt, C::NV, p.status);
+      drain_ring(bar.k_full, cnt, C::NK, p.status);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ Q and dO
+    uint32_t cnt = 0;
+    for (int u = blockIdx.x; u < nitems; u += gridDim.x, ++cnt) {
+      const SwaDqItem w = swa_dq_item(p, u);
+      const uint32_t st = cnt % C::QS;
+      if (!mbar_wait_warp(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2)) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&bar.q_full[st], 2 * T::BYTES);
         swa_load_tile<D>(sbase + C::Q_OFF + st * T::TILE, &tmQ, &tmQ1, &bar.q_full[st], w.qt * kTileRows, w.h, w.b);
         swa_load_tile<D>(sbase + C::DO_OFF + st * T::TILE, &tmG, &tmG1, &bar.q_full[st], w.qt * kTileRows, w.h, w.b);
       }
-      if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
+      __syncwarp();
     }
+    if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // Step by step over the chunks of all items: S and dP of this step as soon as the last
-    // step's have been read into registers, then dQ += dS K of the last step, once dS has been
-    // written back.  The next step's loads are waited for behind the products' issue, where
-    // the tensor core is busy.
-    uint32_t step = 0, qn = 0, an = 0;   // steps, items begun, items whose dQ began
+    // ------------------------------------------------------------ S and dP
+    // Of each chunk, as soon as the last chunk's have been read into registers and the dS
+    // before it has been consumed.
+    uint32_t step = 0, qn = 0;
     bool ok = true;
-    int u = blockIdx.x, m = 0;
-    SwaDqItem w{};
-    bool prev = false, prev_first = false, prev_last = false;
-    auto loads = [&]() {                 // of step `step`, chunk m of item u
-      bool in = true;
-      if (m == 0) in = mbar_wait_warp(&bar.q_full[qn % C::QS], (qn / C::QS) & 1, abort, p.status, site0 + 3);
-      in = in && mbar_wait_warp(&bar.k_full[step % C::NK], (step / C::NK) & 1, abort, p.status, site0 + 4);
-      return in && mbar_wait_warp(&bar.v_full[step % C::NV], (step / C::NV) & 1, abort, p.status, site0 + 5);
-    };
-    if (u < nitems) {
-      w = swa_dq_item(p, u);
-      ok = loads();
-    }
-    while (ok && (u < nitems || prev)) {
-      const bool cur = u < nitems;
-      const uint32_t pstep = step - 1;
-      if (cur) {
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++qn) {
+      const SwaDqItem w = swa_dq_item(p, u);
+      const uint32_t qs = qn % C::QS;
+      if (!(ok = mbar_wait_warp(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
+      for (int m = 0; m < w.nc; ++m, ++step) {
+        const uint32_t vs = step % C::NV, ks = step % C::NK;
+        if (!(ok = mbar_wait_warp(&bar.k_full[ks], (step / C::NK) & 1, abort, p.status, site0 + 4))) break;
+        if (!(ok = mbar_wait_warp(&bar.v_full[vs], (step / C::NV) & 1, abort, p.status, site0 + 5))) break;
+        if (!(ok = mbar_wait_warp(&bar.slot_empty[step & 1], ((step >> 1) & 1) ^ 1, abort, p.status, site0 + 11))) break;
         if (!(ok = mbar_wait_warp(&bar.p_empty[0], (step & 1) ^ 1, abort, p.status, site0 + 10))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t qs = qn % C::QS, vst = step % C::NV;
-          swa_scores<D, 128>(tmem + 128 * (step & 1), base + C::Q_OFF + qs * T::TILE,
-                             base + C::K_OFF + (step % C::NK) * T::TILE, 0);
-          swa_scores<D, 128>(tmem + C::P0, base + C::DO_OFF + qs * T::TILE, base + C::V_OFF + vst * T::TILE, 0);
+          swa_scores<D, 128>(tmem + 128 * (step & 1), base + C::Q_OFF + qs * T::TILE, base + C::K_OFF + ks * T::TILE, 0);
+          swa_scores<D, 128>(tmem + C::P0, base + C::DO_OFF + qs * T::TILE, base + C::V_OFF + vs * T::TILE, 0);
           umma_commit(&bar.s_full[0]);
-          umma_commit(&bar.v_empty[vst]);
+          umma_commit(&bar.v_empty[vs]);
           if (m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
         }
         __syncwarp();
       }
-      const bool pf = prev_first, pl = prev_last, had = prev;
-      prev = cur;
-      prev_first = m == 0;
-      prev_last = m == w.nc - 1;
-      if (cur) {
-        ++step;
-        if (++m == w.nc) {
-          ++qn;
-          m = 0;
-          u += gridDim.x;
-          if (u < nitems) w = swa_dq_item(p, u);
-        }
-        if (u < nitems && !(ok = loads())) break;
-      }
-      if (had) {
-        if (!(ok = mbar_wait_warp(&bar.ds_full[0][pstep & 1], (pstep >> 1) & 1, abort, p.status, site0 + 6))) break;
-        if (pf) {
-          if (!(ok = mbar_wait_warp(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 7))) break;
-          ++an;
-        }
+    }
+    swa_issued(&bar.mma_done[0], p.status);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ dQ += dS K
+    uint32_t step = 0, an = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++an) {
+      const SwaDqItem w = swa_dq_item(p, u);
+      for (int m = 0; m < w.nc; ++m, ++step) {
+        const uint32_t ks = step % C::NK;
+        if (!(ok = mbar_wait_warp(&bar.ds_full[0][step & 1], (step >> 1) & 1, abort, p.status, site0 + 6))) break;
+        if (m == 0 && !(ok = mbar_wait_warp(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 7))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t kt = base + C::K_OFF + (pstep % C::NK) * T::TILE, tS = tmem + 128 * (pstep & 1);
-          swa_acc<D>(tmem + C::ACC, tS, kt, 0, pf);
+          const uint32_t kt = base + C::K_OFF + ks * T::TILE, tS = tmem + 128 * (step & 1);
+          swa_acc<D>(tmem + C::ACC, tS, kt, 0, m == 0);
           swa_acc<D>(tmem + C::ACC, tS + 64, kt, 1, false);
-          umma_commit(&bar.k_empty[pstep % C::NK]);
-          if (pl) umma_commit(&bar.acc_full[0]);
+          umma_commit(&bar.slot_empty[step & 1]);
+          umma_commit(&bar.k_empty[ks]);
+          if (m == w.nc - 1) umma_commit(&bar.acc_full[0]);
         }
         __syncwarp();
       }
     }
-    if (elect_one()) {
-      umma_commit(&bar.mma_done);
-      const unsigned long long t0 = global_timer_ns();
-      while (!mbar_try_wait(&bar.mma_done, 0) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
-    }
+    swa_issued(&bar.mma_done[1], p.status);
   } else {
     // ------------------------------------------------------------ dS, and dQ out
     // Group grp takes the columns [64 grp, 64 grp + 64) of S and dP.  An item's dQ is read
     // out behind the first chunk of the next item, when its last product is long done.
-    const int q4 = warp & 3, grp = (warp - 2) >> 2;
+    const int q4 = warp & 3, grp = (warp - 4) >> 2;
     const int r = 32 * q4 + lane;                   // row == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
     const uint32_t tP = tmem + lane_off + C::P0 + 64 * grp;
@@ -414,8 +420,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     uint16_t *dst = nullptr;                        // the last item's row of dQ
     bool live = false, pend = false;
     auto read_out = [&]() {
-      bool in = mbar_wait(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9);
-      if (!__all_sync(FULL, in)) return false;
+      if (!mbar_wait_warp(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9)) return false;
       ++an;
       tc_fence_after();
       // A lane's 16 columns are one whole 32-byte sector of its row.
@@ -439,8 +444,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const float *st = p.stat + (((int64_t)w.b * p.hq + w.h) * p.nt + w.qt) * 256 + r;
       const float nl = st[0], nd = st[128];
       for (int m = 0; m < w.nc; ++m, ++sc) {
-        ok = mbar_wait(&bar.s_full[0], sc & 1, abort, p.status, site0 + 8);
-        if (!(ok = __all_sync(FULL, ok))) break;
+        if (!(ok = mbar_wait_warp(&bar.s_full[0], sc & 1, abort, p.status, site0 + 8))) break;
         tc_fence_after();
         const int key0 = swa_dq_key(w, m) + 64 * grp;
         const bool full = key0 + 63 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 64 <= p.sink);
@@ -548,9 +552,9 @@ __device__ __forceinline__ bool swa_dkv_unit(const SwaBwdParams &p, int u, SwaDk
 
 // TMEM of the dK / dV kernel: the halves' S in a ring of `S` slots of 64 columns (P and dS
 // are written back over them), their dP in a ring of two, then the accumulators.  With
-// three S slots a half's products are issued as soon as the half before the last has been
-// read into registers, while its group still computes; dK and dV of 128 columns leave room
-// for two, and a half's products wait for its group's write-back.
+// three S slots a half's products are issued as soon as its group has read its last half
+// into registers, while it still computes; dK and dV of 128 columns leave room for two, and
+// a half's products wait for its group's write-back.
 template <int SLOTS>
 struct SwaTmem {
   static constexpr int S = SLOTS;
@@ -611,130 +615,122 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   volatile int *abort = &bar.abort;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- K and V
-      uint32_t cnt = 0;
-      for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
-        SwaDkvUnit w;
-        if (!swa_dkv_unit(p, u, w)) continue;
-        const uint32_t st = cnt % C::KS;
-        if (!mbar_wait(&bar.k_empty[st], ((cnt / C::KS) & 1) ^ 1, abort, p.status, site0 + 1)) break;
+    // ------------------------------------------------------------ K and V
+    uint32_t cnt = 0;
+    for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
+      SwaDkvUnit w;
+      if (!swa_dkv_unit(p, u, w)) continue;
+      const uint32_t st = cnt % C::KS;
+      if (!mbar_wait_warp(&bar.k_empty[st], ((cnt / C::KS) & 1) ^ 1, abort, p.status, site0 + 1)) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&bar.k_full[st], 2 * T::BYTES);
         swa_load_tile<D>(sbase + C::K_OFF + st * T::TILE, &tmK, &tmK1, &bar.k_full[st], w.kt * kTileKeys, w.hk, w.b);
         swa_load_tile<D>(sbase + C::V_OFF + st * T::TILE, &tmV, &tmV1, &bar.k_full[st], w.kt * kTileKeys, w.hk, w.b);
-        ++cnt;
       }
-      if (*abort) drain_ring(bar.k_full, cnt, C::KS, p.status);
-    } else if (lane == 1) {
-      // ---------------------------------------------------------- Q, dO, row statistics
-      uint32_t cnt = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
-        SwaDkvUnit w;
-        if (!swa_dkv_unit(p, u, w)) continue;
-        int g = w.t0 / w.len, qt = w.first + w.t0 % w.len;
-        for (int t = w.t0; t < w.t1; ++t, ++cnt) {
-          const uint32_t st = cnt % C::QS;
-          if (!(ok = mbar_wait(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2))) break;
+      __syncwarp();
+      ++cnt;
+    }
+    if (*abort) drain_ring(bar.k_full, cnt, C::KS, p.status);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ Q, dO, row statistics
+    uint32_t cnt = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
+      SwaDkvUnit w;
+      if (!swa_dkv_unit(p, u, w)) continue;
+      int g = w.t0 / w.len, qt = w.first + w.t0 % w.len;
+      for (int t = w.t0; t < w.t1; ++t, ++cnt) {
+        const uint32_t st = cnt % C::QS;
+        if (!(ok = mbar_wait_warp(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2))) break;
+        if (elect_one()) {
           const int h = w.hk * p.G + g;
           mbar_arrive_expect_tx(&bar.q_full[st], 2 * T::BYTES + 1024);
           swa_load_tile<D>(sbase + C::Q_OFF + st * T::TILE, &tmQ, &tmQ1, &bar.q_full[st], qt * kTileRows, h, w.b);
           swa_load_tile<D>(sbase + C::DO_OFF + st * T::TILE, &tmG, &tmG1, &bar.q_full[st], qt * kTileRows, h, w.b);
           bulk_load(sbase + C::ST_OFF + st * 1024, p.stat + (((int64_t)w.b * p.hq + h) * p.nt + qt) * 256, 1024,
                     &bar.q_full[st]);
-          if (++qt == w.first + w.len) {
-            qt = w.first;
-            ++g;
-          }
+        }
+        __syncwarp();
+        if (++qt == w.first + w.len) {
+          qt = w.first;
+          ++g;
         }
       }
-      if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
     }
+    if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // Step by step over the query tiles of all units, per half x: S^T_x and dP^T_x of this
-    // step, and dV += P^T_x dO_x, dK += dS^T_x Q_x of the last step; with two S slots the
-    // last step's come first, since they free the slot.
+    // ------------------------------------------------------------ S^T and dP^T
+    // Per query tile and half x, as soon as its group has read its last half's into
+    // registers and the S slot's write-back has been consumed.
     using M = typename C::M;
-    uint32_t step = 0, kn = 0, an = 0;
+    uint32_t step = 0, kn = 0;
     bool ok = true;
-    SwaDkvUnit w{};
-    auto seek = [&](int v) {
-      while (v < nunits && !swa_dkv_unit(p, v, w)) v += gridDim.x;
-      return v;
-    };
-    int u = seek(blockIdx.x), t = w.t0;
-    bool prev = false, prev_first = false, prev_last = false;
-    const uint32_t tK = tmem + M::ACC, tV = tK + D;
-    while (ok && (u < nunits || prev)) {
-      const bool cur = u < nunits;
-      const uint32_t st = step % C::QS, pst = (step - 1) % C::QS, ks = kn % C::KS;
-      const bool last = t == w.t1 - 1;
-      if (cur) {
-        if (t == w.t0 && !(ok = mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3))) break;
+    for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
+      SwaDkvUnit w;
+      if (!swa_dkv_unit(p, u, w)) continue;
+      const uint32_t ks = kn % C::KS;
+      if (!(ok = mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3))) break;
+      ++kn;
+      const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
+      for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
+        const uint32_t st = step % C::QS;
         if (!(ok = mbar_wait_warp(&bar.q_full[st], (step / C::QS) & 1, abort, p.status, site0 + 4))) break;
-      }
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int x = y >> 1;
-        const uint32_t h = 2 * step + x;
-        if (((y & 1) == 0) == (M::S == 3)) {
-          if (!cur) continue;
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t h = 2 * step + x;
+          if (!(ok = mbar_wait_warp(&bar.slot_empty[h % M::S], ((h / M::S) & 1) ^ 1, abort, p.status, site0 + 11))) break;
           if (!(ok = mbar_wait_warp(&bar.p_empty[x], (step & 1) ^ 1, abort, p.status, site0 + 10))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
             swa_scores<D, 64>(tmem + M::s_at(h), kt, base + C::Q_OFF + st * T::TILE, 64 * x);
             swa_scores<D, 64>(tmem + M::P0 + 64 * x, vt, base + C::DO_OFF + st * T::TILE, 64 * x);
             umma_commit(&bar.s_full[x]);
-            if (x == 1 && last) umma_commit(&bar.k_empty[ks]);
+            if (x == 1 && t == w.t1 - 1) umma_commit(&bar.k_empty[ks]);
           }
           __syncwarp();
-        } else {
-          if (!prev) continue;
-          if (!(ok = mbar_wait_warp(&bar.ds_full[x][(step - 1) & 1], ((step - 1) >> 1) & 1, abort, p.status, site0 + 5))) break;
-          if (x == 0 && prev_first) {
+        }
+      }
+    }
+    swa_issued(&bar.mma_done[0], p.status);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ dV += P^T dO, dK += dS^T Q
+    using M = typename C::M;
+    const uint32_t tK = tmem + M::ACC, tV = tK + D;
+    uint32_t step = 0, an = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
+      SwaDkvUnit w;
+      if (!swa_dkv_unit(p, u, w)) continue;
+      for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
+        const uint32_t st = step % C::QS;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t h = 2 * step + x;
+          if (!(ok = mbar_wait_warp(&bar.ds_full[x][step & 1], (step >> 1) & 1, abort, p.status, site0 + 5))) break;
+          if (x == 0 && t == w.t0) {
             if (!(ok = mbar_wait_warp(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 6))) break;
             ++an;
           }
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t qp = base + C::Q_OFF + pst * T::TILE, gp = base + C::DO_OFF + pst * T::TILE;
-            const uint32_t tS = tmem + M::s_at(h - 2);   // P^T, then dS^T
-            swa_acc<D>(tV, tS, gp, x, prev_first && x == 0);
-            swa_acc<D>(tK, tS + 32, qp, x, prev_first && x == 0);
+            const uint32_t qp = base + C::Q_OFF + st * T::TILE, gp = base + C::DO_OFF + st * T::TILE;
+            const uint32_t tS = tmem + M::s_at(h);   // P^T, then dS^T
+            swa_acc<D>(tV, tS, gp, x, x == 0 && t == w.t0);
+            swa_acc<D>(tK, tS + 32, qp, x, x == 0 && t == w.t0);
+            umma_commit(&bar.slot_empty[h % M::S]);
             if (x == 1) {
-              umma_commit(&bar.q_empty[pst]);
-              if (prev_last) umma_commit(&bar.acc_full[0]);
+              umma_commit(&bar.q_empty[st]);
+              if (t == w.t1 - 1) umma_commit(&bar.acc_full[0]);
             }
           }
           __syncwarp();
         }
       }
-      if (!ok) break;
-      prev = cur;
-      if (cur) {
-        prev_first = t == w.t0;
-        prev_last = last;
-        ++step;
-        ++t;
-        if (last) {
-          ++kn;
-          u = seek(u + gridDim.x);
-          t = w.t0;
-        }
-      } else {
-        break;
-      }
     }
-    if (elect_one()) {
-      umma_commit(&bar.mma_done);
-      const unsigned long long t0 = global_timer_ns();
-      while (!mbar_try_wait(&bar.mma_done, 0) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
-    }
+    swa_issued(&bar.mma_done[1], p.status);
   } else {
     // ------------------------------------------------------------ P^T, dS^T; dK, dV out
-    const int q4 = warp & 3, grp = (warp - 2) >> 2;
+    const int q4 = warp & 3, grp = (warp - 4) >> 2;
     const int r = 32 * q4 + lane;                   // key of the tile == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
     using M = typename C::M;
@@ -750,10 +746,8 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       int qt = w.first + w.t0 % w.len;
       for (int t = w.t0; t < w.t1; ++t, ++sc) {
         const uint32_t st = sc % C::QS;
-        ok = mbar_wait(&bar.q_full[st], (sc / C::QS) & 1, abort, p.status, site0 + 7);
-        if (!(ok = __all_sync(FULL, ok))) break;
-        ok = mbar_wait(&bar.s_full[grp], sc & 1, abort, p.status, site0 + 8);
-        if (!(ok = __all_sync(FULL, ok))) break;
+        if (!(ok = mbar_wait_warp(&bar.q_full[st], (sc / C::QS) & 1, abort, p.status, site0 + 7))) break;
+        if (!(ok = mbar_wait_warp(&bar.s_full[grp], sc & 1, abort, p.status, site0 + 8))) break;
         tc_fence_after();
         const float *nl = reinterpret_cast<const float *>(sbase + C::ST_OFF + st * 1024) + 64 * grp;
         const int i0 = qt * kTileRows + 64 * grp;   // row of the group's first column
@@ -807,8 +801,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         if (lane == 0) mbar_arrive(&bar.ds_full[grp][sc & 1]);
       }
       if (!ok) break;
-      ok = mbar_wait(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9);
-      if (!(ok = __all_sync(FULL, ok))) break;
+      if (!(ok = mbar_wait_warp(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9))) break;
       ++an;
       tc_fence_after();
       // Group 0 writes dK, group 1 dV.
