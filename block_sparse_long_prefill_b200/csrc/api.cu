@@ -745,6 +745,7 @@ int swa_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, m
   p.dv_sb = dv.sb; p.dv_sh = dv.sh; p.dv_sn = dv.sn;
   char *ws = static_cast<char *>(workspace);
   p.stat = reinterpret_cast<float *>(ws);
+  p.extra = reinterpret_cast<uint16_t *>(ws + plan.off_extra);
   p.part = reinterpret_cast<float *>(ws + plan.off_part);
   p.batch = batch; p.hq = hq; p.hkv = hkv; p.N = N; p.d = d;
   p.window = w;

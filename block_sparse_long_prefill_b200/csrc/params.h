@@ -293,6 +293,8 @@ struct SwaBwdParams {
   int64_t dq_sb, dq_sh, dq_sn, dk_sb, dk_sh, dk_sn, dv_sb, dv_sh, dv_sn;
   float *stat;             // [batch, hq, nt, 2, 128]: -lse * log2(e), -D = -dO . o of a tile's
                            // rows (behind row N: -inf, 0)
+  uint16_t *extra;         // [batch, hq, nt, 128, 16]: the same statistics as bf16 columns of
+                           // the products (swizzled rows of 32 bytes)
   float *part;             // dK, dV of the sinks' key tiles in parts:
                            // [batch, hkv, nst, 1 + nseg, 2, 128, D]
   int batch, hq, hkv, N, d, window, sink, G;
@@ -314,7 +316,7 @@ __host__ __device__ inline int swa_last_tile(int kt, int window, int nt) {
 // part is much longer than a band's walk.
 struct SwaBwdPlan {
   int nt, nst, seg, nseg;
-  size_t off_part, total;
+  size_t off_extra, off_part, total;
 };
 
 inline SwaBwdPlan swa_bwd_plan(int batch, int hq, int hkv, int N, int d, int window, int sink) {
@@ -335,6 +337,8 @@ inline SwaBwdPlan swa_bwd_plan(int batch, int hq, int hkv, int N, int d, int win
     w.nseg = (int)((far0 + seg - 1) / seg);
   }
   size_t off = align_up(size_t(batch) * hq * w.nt * 2 * kTileRows * 4, 1024);
+  w.off_extra = off;
+  off = align_up(off + size_t(batch) * hq * w.nt * kTileRows * 32, 1024);
   w.off_part = off;
   off += size_t(batch) * hkv * w.nst * (1 + w.nseg) * 2 * kTileKeys * d * 4;
   w.total = align_up(off, 256);

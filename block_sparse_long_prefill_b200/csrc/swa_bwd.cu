@@ -10,7 +10,8 @@
 // (a KV head's dK and dV sum over the q-heads that read it).  No atomics: every sum has one
 // order, so results repeat bit for bit.
 //
-//   swa_bwd_prep_kernel   per row -lse log2(e) and -D, in the tiles' order; HBM-bound
+//   swa_bwd_prep_kernel   per row -lse log2(e) and -D, in the tiles' order, and the same two
+//                         as columns for the products of the dK / dV kernel; HBM-bound
 //   swa_bwd_dq_kernel     query-stationary: a 128-row tile walks its key chunks (the sinks'
 //                         chunks before the band, then the band): S = Q K^T, dP = dO V^T,
 //                         dS = P (dP - D) on the CUDA cores, dQ += dS K in TMEM; written once
@@ -81,8 +82,10 @@ __device__ __forceinline__ void swa_acc(uint32_t d, uint32_t a, uint32_t tile, i
 }
 
 // S (NB columns) = A B^T over the D columns; A and B K-major tiles, B's NB rows from row0 on.
+// extra_a, extra_b: blocks of 16 more columns (32-byte rows, 32-byte swizzle), or 0.
 template <int D, int NB>
-__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int row0) {
+__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int row0, uint32_t extra_a = 0,
+                                           uint32_t extra_b = 0) {
   constexpr uint32_t id = idesc_bf16(128, NB, 0, 0);
   const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16) + row0 * 8;
 #pragma unroll
@@ -94,6 +97,7 @@ __device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, i
       umma_ss_w(d, al + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128,
                 bl + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128, id, acc);
   }
+  if (extra_a) umma_ss_w(d, desc_lo(extra_a, 16), kHi32, desc_lo(extra_b, 16) + row0 * 2, kHi32, id, 1u);
 }
 
 template <int D>
@@ -103,7 +107,7 @@ __device__ __forceinline__ void swa_load_tile(unsigned char *dst, const CUtensor
   if (D != 64) tma_load_4d(dst + SwaTile<D>::R0, m1, bar, 64, row, h, b);
 }
 
-// Bulk copy of a tile's row statistics (1 KB, 16-byte aligned on both sides).
+// Bulk copy (16-byte aligned on both sides).
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -121,18 +125,53 @@ __device__ __forceinline__ void drain_ring(uint64_t *full, uint32_t cnt, uint32_
 
 // Packed fp32 pairs, each lane rounded as the scalar instruction would.
 __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b, float c0, float c1) {
-  asm("{.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;}"
-      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+  const float2 d = __ffma2_rn(make_float2(a0, a1), make_float2(b, b), make_float2(c0, c1));
+  d0 = d.x;
+  d1 = d.y;
+}
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+  const float2 d = __fmul2_rn(make_float2(a0, a1), make_float2(b0, b1));
+  d0 = d.x;
+  d1 = d.y;
 }
 // d = p * (v + c) on pairs.
 __device__ __forceinline__ void addmul2(float &d0, float &d1, float v0, float v1, float c0, float c1,
                                         float p0, float p1) {
-  asm("{.reg .b64 rv, rc, rp, rd;\n\t"
-      "mov.b64 rv, {%2, %3};\n\tmov.b64 rc, {%4, %5};\n\tmov.b64 rp, {%6, %7};\n\t"
-      "add.rn.f32x2 rd, rv, rc;\n\tmul.rn.f32x2 rd, rd, rp;\n\tmov.b64 {%0, %1}, rd;}"
-      : "=f"(d0), "=f"(d1) : "f"(v0), "f"(v1), "f"(c0), "f"(c1), "f"(p0), "f"(p1));
+  const float2 d = __fmul2_rn(__fadd2_rn(make_float2(v0, v1), make_float2(c0, c1)), make_float2(p0, p1));
+  d0 = d.x;
+  d1 = d.y;
+}
+
+// The n lowest of 32 bits (n below 0: none, above 32: all).
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+// Bits e and e + 1 of b as the halves of a packed pair.
+__device__ __forceinline__ uint32_t pair_mask(uint32_t b, int e) {
+  return ((b >> e) & 1u ? 0x0000FFFFu : 0u) | ((b >> (e + 1)) & 1u ? 0xFFFF0000u : 0u);
+}
+
+// The statistics of a query tile as 16 more columns of its Q and dO (dK / dV kernel): there
+// a thread holds a key and every query of the tile, so -lse / scale and -D would have to come
+// through shared memory for each of them (measured: 1024 cycles a tile of shared-memory
+// bandwidth that the products need).  Instead S^T - lse / scale and dP^T - D come out of
+// the products: the columns hold each value in three bf16 terms (2^-24 of it left over),
+// against a constant block of ones in the columns of the value that is wanted.
+// A block: 128 rows of 32 bytes with the 32-byte swizzle, 4 KB.
+constexpr int kSwaExtra = 128 * 32;
+
+__device__ __forceinline__ uint32_t extra_offset(int row, int chunk) {
+  return row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4);
+}
+
+// x = t0 + t1 + t2 in bf16 (bits), up to 2^-24 of it.
+__device__ __forceinline__ void split3(float x, uint32_t *t) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t h = pack_bf16x2(x, 0.f) & 0xFFFFu;
+    t[i] = h;
+    x -= __uint_as_float(h << 16);
+  }
 }
 
 // ------------------------------------------------------------------ prep
@@ -164,8 +203,18 @@ __global__ void __launch_bounds__(256) swa_bwd_prep_kernel(const SwaBwdParams p)
     acc = row_sum<D>(acc, base, vv);
     if (in && v == 0 && i < padded) {
       float *st = p.stat + (bh * p.nt + i / kTileRows) * 256 + (i & 127);
-      st[0] = live ? -p.lse[bh * p.N + i] * 1.4426950408889634f : -INFINITY;
+      const float lse = live ? p.lse[bh * p.N + i] : 0.f;
+      st[0] = live ? -lse * 1.4426950408889634f : -INFINITY;
       st[128] = live ? -acc : 0.f;
+      // (Rows behind the last: far below every score, and finite, since the other product
+      // multiplies it by zero.)
+      uint32_t t[6];
+      split3(live ? -lse / p.scale : -1e30f, t);
+      split3(live ? -acc : 0.f, t + 3);
+      unsigned char *blk = reinterpret_cast<unsigned char *>(p.extra + (bh * p.nt + i / kTileRows) * (kSwaExtra / 2));
+      *reinterpret_cast<uint4 *>(blk + extra_offset(i & 127, 0)) =
+          make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, 0u);
+      *reinterpret_cast<uint4 *>(blk + extra_offset(i & 127, 1)) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
 }
@@ -200,8 +249,8 @@ struct SwaDqCfg {
   static constexpr int QS = D == 128 ? 1 : 2;              // Q / dO stages
   static constexpr int NK = D == 128 ? 3 : (D == 80 ? 4 : 5);  // K stages (held until dQ)
   static constexpr int NV = D == 128 ? 2 : (D == 80 ? 3 : 4);  // V stages
-  // TMEM: two S slots of 128 columns (dS is written back over them), dP, dQ.
-  static constexpr uint32_t P0 = 256, ACC = 384;
+  // TMEM: S, dP, two dS slots of 64 columns, dQ.
+  static constexpr uint32_t P0 = 128, DS0 = 256, ACC = 384;
   static constexpr int Q_OFF = 0;
   static constexpr int DO_OFF = QS * SwaTile<D>::TILE;
   static constexpr int K_OFF = 2 * QS * SwaTile<D>::TILE;
@@ -218,7 +267,7 @@ struct SwaBars {
   // back, of even and odd steps: a step's products are issued before the last step's
   // write-back is waited for, so two write-backs may complete before that wait looks.
   uint64_t s_full[2], p_empty[2], ds_full[2][2];
-  uint64_t slot_empty[3];              // the S slot's write-back consumed
+  uint64_t slot_empty[3];              // a write-back's slot consumed
   uint64_t acc_full[2], acc_empty[2];  // accumulators final / read out
   uint64_t mma_done[2];                // per issuing warp
   uint32_t tmem_base;
@@ -357,8 +406,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S and dP
-    // Of each chunk, as soon as the last chunk's have been read into registers and the dS
-    // before it has been consumed.
+    // Of each chunk, as soon as the last chunk's have been read into registers.
     uint32_t step = 0, qn = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++qn) {
@@ -369,11 +417,10 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const uint32_t vs = step % C::NV, ks = step % C::NK;
         if (!(ok = mbar_wait_warp(&bar.k_full[ks], (step / C::NK) & 1, abort, p.status, site0 + 4))) break;
         if (!(ok = mbar_wait_warp(&bar.v_full[vs], (step / C::NV) & 1, abort, p.status, site0 + 5))) break;
-        if (!(ok = mbar_wait_warp(&bar.slot_empty[step & 1], ((step >> 1) & 1) ^ 1, abort, p.status, site0 + 11))) break;
         if (!(ok = mbar_wait_warp(&bar.p_empty[0], (step & 1) ^ 1, abort, p.status, site0 + 10))) break;
         tc_fence_after();
         if (elect_one()) {
-          swa_scores<D, 128>(tmem + 128 * (step & 1), base + C::Q_OFF + qs * T::TILE, base + C::K_OFF + ks * T::TILE, 0);
+          swa_scores<D, 128>(tmem, base + C::Q_OFF + qs * T::TILE, base + C::K_OFF + ks * T::TILE, 0);
           swa_scores<D, 128>(tmem + C::P0, base + C::DO_OFF + qs * T::TILE, base + C::V_OFF + vs * T::TILE, 0);
           umma_commit(&bar.s_full[0]);
           umma_commit(&bar.v_empty[vs]);
@@ -395,9 +442,9 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (m == 0 && !(ok = mbar_wait_warp(&bar.acc_empty[0], (an & 1) ^ 1, abort, p.status, site0 + 7))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t kt = base + C::K_OFF + ks * T::TILE, tS = tmem + 128 * (step & 1);
+          const uint32_t kt = base + C::K_OFF + ks * T::TILE, tS = tmem + C::DS0 + 64 * (step & 1);
           swa_acc<D>(tmem + C::ACC, tS, kt, 0, m == 0);
-          swa_acc<D>(tmem + C::ACC, tS + 64, kt, 1, false);
+          swa_acc<D>(tmem + C::ACC, tS + 32, kt, 1, false);
           umma_commit(&bar.slot_empty[step & 1]);
           umma_commit(&bar.k_empty[ks]);
           if (m == w.nc - 1) umma_commit(&bar.acc_full[0]);
@@ -448,7 +495,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_after();
         const int key0 = swa_dq_key(w, m) + 64 * grp;
         const bool full = key0 + 63 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 64 <= p.sink);
-        const uint32_t tS = tmem + lane_off + 128 * (sc & 1) + 64 * grp;
+        const uint32_t tS = tmem + lane_off + 64 * grp, tD = tmem + lane_off + C::DS0 + 64 * (sc & 1) + 32 * grp;
         uint32_t sv[64], pv[64];
         tmem_ld64(tS, sv);
         tmem_ld64(tP, pv);
@@ -456,6 +503,8 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_empty[0]);
+        // The dS slot's last product is done (it was issued a step ago).
+        if (!(ok = mbar_wait_warp(&bar.slot_empty[sc & 1], ((sc >> 1) & 1) ^ 1, abort, p.status, site0 + 11))) break;
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t ds[16];
@@ -469,14 +518,12 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           }
           if (!full) {
             // Keys that the row does not see: zero halves of the packed pairs.
+            const uint32_t b = first_bits(i + 1 - key0 - c) &
+                               (~first_bits(i + 1 - p.window - key0 - c) | first_bits(p.sink - key0 - c));
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const int k0 = key0 + c + e, k1 = k0 + 1;
-              if (k0 > i || (i - k0 >= p.window && k0 >= p.sink)) ds[e / 2] &= 0xFFFF0000u;
-              if (k1 > i || (i - k1 >= p.window && k1 >= p.sink)) ds[e / 2] &= 0x0000FFFFu;
-            }
+            for (int e = 0; e < 32; e += 2) ds[e / 2] &= pair_mask(b, e);
           }
-          tmem_st16(tS + c / 2, ds);
+          tmem_st16(tD + c / 2, ds);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -570,8 +617,9 @@ struct SwaDkvCfg {
   static constexpr int V_OFF = KS * SwaTile<D>::TILE;
   static constexpr int Q_OFF = 2 * KS * SwaTile<D>::TILE;
   static constexpr int DO_OFF = Q_OFF + QS * SwaTile<D>::TILE;
-  static constexpr int ST_OFF = DO_OFF + QS * SwaTile<D>::TILE;
-  static constexpr int BAR_OFF = ST_OFF + QS * 1024;
+  static constexpr int EX_OFF = DO_OFF + QS * SwaTile<D>::TILE;   // a stage's statistics columns
+  static constexpr int ONE_OFF = EX_OFF + QS * kSwaExtra;         // ones: lse's columns, D's
+  static constexpr int BAR_OFF = ONE_OFF + 2 * kSwaExtra;
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
   using M = SwaTmem<D == 128 ? 2 : 3>;
@@ -598,6 +646,14 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const int nunits = swa_dkv_units(p);
 
   if (tid == 0) swa_init_bars(bar, 4);
+  // The blocks of ones: columns 0 - 2 (lse) and 3 - 5 (D).
+  for (int r = tid; r < 2 * 128; r += kSwaBwdThreads) {
+    unsigned char *blk = sbase + C::ONE_OFF + (r >> 7) * kSwaExtra;
+    const uint4 ones = r < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u);
+    *reinterpret_cast<uint4 *>(blk + extra_offset(r & 127, 0)) = ones;
+    *reinterpret_cast<uint4 *>(blk + extra_offset(r & 127, 1)) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmG);
@@ -644,11 +700,11 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         if (!(ok = mbar_wait_warp(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2))) break;
         if (elect_one()) {
           const int h = w.hk * p.G + g;
-          mbar_arrive_expect_tx(&bar.q_full[st], 2 * T::BYTES + 1024);
+          mbar_arrive_expect_tx(&bar.q_full[st], 2 * T::BYTES + kSwaExtra);
           swa_load_tile<D>(sbase + C::Q_OFF + st * T::TILE, &tmQ, &tmQ1, &bar.q_full[st], qt * kTileRows, h, w.b);
           swa_load_tile<D>(sbase + C::DO_OFF + st * T::TILE, &tmG, &tmG1, &bar.q_full[st], qt * kTileRows, h, w.b);
-          bulk_load(sbase + C::ST_OFF + st * 1024, p.stat + (((int64_t)w.b * p.hq + h) * p.nt + qt) * 256, 1024,
-                    &bar.q_full[st]);
+          bulk_load(sbase + C::EX_OFF + st * kSwaExtra,
+                    p.extra + (((int64_t)w.b * p.hq + h) * p.nt + qt) * (kSwaExtra / 2), kSwaExtra, &bar.q_full[st]);
         }
         __syncwarp();
         if (++qt == w.first + w.len) {
@@ -673,7 +729,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ++kn;
       const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
       for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
-        const uint32_t st = step % C::QS;
+        const uint32_t st = step % C::QS, ex = base + C::EX_OFF + st * kSwaExtra;
         if (!(ok = mbar_wait_warp(&bar.q_full[st], (step / C::QS) & 1, abort, p.status, site0 + 4))) break;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -682,8 +738,9 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           if (!(ok = mbar_wait_warp(&bar.p_empty[x], (step & 1) ^ 1, abort, p.status, site0 + 10))) break;
           tc_fence_after();
           if (elect_one()) {
-            swa_scores<D, 64>(tmem + M::s_at(h), kt, base + C::Q_OFF + st * T::TILE, 64 * x);
-            swa_scores<D, 64>(tmem + M::P0 + 64 * x, vt, base + C::DO_OFF + st * T::TILE, 64 * x);
+            swa_scores<D, 64>(tmem + M::s_at(h), kt, base + C::Q_OFF + st * T::TILE, 64 * x, base + C::ONE_OFF, ex);
+            swa_scores<D, 64>(tmem + M::P0 + 64 * x, vt, base + C::DO_OFF + st * T::TILE, 64 * x,
+                              base + C::ONE_OFF + kSwaExtra, ex);
             umma_commit(&bar.s_full[x]);
             if (x == 1 && t == w.t1 - 1) umma_commit(&bar.k_empty[ks]);
           }
@@ -745,11 +802,8 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       const int key0 = w.kt * kTileKeys, key = key0 + r;
       int qt = w.first + w.t0 % w.len;
       for (int t = w.t0; t < w.t1; ++t, ++sc) {
-        const uint32_t st = sc % C::QS;
-        if (!(ok = mbar_wait_warp(&bar.q_full[st], (sc / C::QS) & 1, abort, p.status, site0 + 7))) break;
         if (!(ok = mbar_wait_warp(&bar.s_full[grp], sc & 1, abort, p.status, site0 + 8))) break;
         tc_fence_after();
-        const float *nl = reinterpret_cast<const float *>(sbase + C::ST_OFF + st * 1024) + 64 * grp;
         const int i0 = qt * kTileRows + 64 * grp;   // row of the group's first column
         const bool full = key0 + kTileKeys - 1 <= i0 && (i0 + 63 - key0 < p.window || key0 + kTileKeys <= p.sink);
         if (++qt == w.first + w.len) qt = w.first;
@@ -765,29 +819,22 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         for (int c = 0; c < 64; c += 32) {
           uint32_t pp[16], dd[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4 *>(nl + c + e);
-            const float4 d4 = *reinterpret_cast<const float4 *>(nl + 128 + c + e);
-            const float *sf = reinterpret_cast<const float *>(sv + c + e), *pf = reinterpret_cast<const float *>(pv + c + e);
-            float pr[4], ds[4];
-            fma2(pr[0], pr[1], sf[0], sf[1], sl2, l4.x, l4.y);
-            fma2(pr[2], pr[3], sf[2], sf[3], sl2, l4.z, l4.w);
-#pragma unroll
-            for (int f = 0; f < 4; ++f) pr[f] = ex2_approx(pr[f]);
-            addmul2(ds[0], ds[1], pf[0], pf[1], d4.x, d4.y, pr[0], pr[1]);
-            addmul2(ds[2], ds[3], pf[2], pf[3], d4.z, d4.w, pr[2], pr[3]);
-            pp[e / 2] = pack_bf16x2(pr[0], pr[1]);
-            pp[e / 2 + 1] = pack_bf16x2(pr[2], pr[3]);
-            dd[e / 2] = pack_bf16x2(ds[0], ds[1]);
-            dd[e / 2 + 1] = pack_bf16x2(ds[2], ds[3]);
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1, d0, d1;
+            mul2(x0, x1, __uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1]), sl2, sl2);
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            mul2(d0, d1, __uint_as_float(pv[c + e]), __uint_as_float(pv[c + e + 1]), x0, x1);
+            pp[e / 2] = pack_bf16x2(x0, x1);
+            dd[e / 2] = pack_bf16x2(d0, d1);
           }
           if (!full) {
             // Rows that do not see the key: zero halves of the packed pairs.
+            const uint32_t b = ~first_bits(key - i0 - c) &
+                               (first_bits(key + p.window - i0 - c) | (key < p.sink ? 0xFFFFFFFFu : 0u));
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const int ia = i0 + c + e, ib = ia + 1;
-              const uint32_t keep = ((key > ia || (ia - key >= p.window && key >= p.sink)) ? 0u : 0x0000FFFFu) |
-                                    ((key > ib || (ib - key >= p.window && key >= p.sink)) ? 0u : 0xFFFF0000u);
+              const uint32_t keep = pair_mask(b, e);
               pp[e / 2] &= keep;
               dd[e / 2] &= keep;
             }
