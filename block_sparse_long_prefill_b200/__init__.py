@@ -143,19 +143,20 @@ def _device(fn: str, *specs):
     for name, t, dt, contig, shape in specs:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        i = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if i < 0:
             raise ValueError(f"{fn}: {name} must be a CUDA tensor")
         if dt is not None and t.dtype != dt:
             raise ValueError(f"{fn}: {name} must be {dt}, not {t.dtype}")
         if contig and not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{fn}: every tensor must be on {dev}; {name} is on {t.device}")
-    return dev
+            dev = i
+        elif i != dev:
+            raise ValueError(f"{fn}: every tensor must be on cuda:{dev}; {name} is on {t.device}")
+    return None if dev is None else torch.device("cuda", dev)
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -164,10 +165,11 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 @contextlib.contextmanager
-def _on(dev, stream):
-    """Makes ``dev`` the current device and ``stream`` (None: the device's current one) its
-    current stream, so that what a wrapper allocates belongs to the stream that uses it."""
+def _moved(dev, stream):
     with torch.cuda.device(dev):
         if stream is None:
             yield
@@ -176,8 +178,16 @@ def _on(dev, stream):
                 yield
 
 
+def _on(dev, stream):
+    """Makes ``dev`` the current device and ``stream`` (None: the device's current one) its
+    current stream, so that what a wrapper allocates belongs to the stream that uses it."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return _HERE_ALREADY
+    return _moved(dev, stream)
+
+
 def _empty(shape, dtype, dev):
-    return torch.empty(tuple(shape), dtype=dtype, device=dev)
+    return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _ptr(x):
@@ -296,7 +306,7 @@ def swa_attn_fwd_chunk(q, k, v, window: int, scale: float = 0.0, out=None, lse=N
                   ("v", v, _BF16, False, tuple(k.shape)),
                   ("out", out, _BF16, False, tuple(q.shape)),
                   ("lse", lse, _F32, True, (b, hq, N)))
-    with torch.cuda.device(dev):
+    with _on(dev, None):
         if out is None:
             out = torch.empty_like(q)
         if lse is None:

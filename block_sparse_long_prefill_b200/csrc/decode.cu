@@ -7,10 +7,13 @@
 //
 // Every visible key and value is read once and used for the G query heads of its KV head,
 // so the work is HBM-bound (4 G flops a byte at most).  The keys of a (sequence, KV head,
-// group of up to 16 query heads) -- an item -- are cut into tiles of 16, and all tiles of
-// the batch are dealt out in equal runs to a grid of two CTAs per SM, whatever the
+// group of up to 16 query heads) -- an item -- are cut into tiles of 16, and the work of
+// the batch is dealt out in equal runs to a grid of two CTAs per SM, whatever the
 // sequences' lengths: a run may end inside an item, which then has partial results
-// (normalised rows and their log-sum-exp) that a second, small kernel joins.
+// (normalised rows and their log-sum-exp) that a second, small kernel joins.  An item counts
+// as its tiles and kDecItem more, about what filling the pipeline and joining the warps
+// costs: by tiles alone a run of many one-tile items took six times as long as one of few
+// long items.
 //
 // A warp takes every fourth tile of its CTA's run and works alone: its tiles arrive by
 // cp.async in a ring of its own (three stages of 16 keys and 16 values, about 9 KB each,
@@ -35,6 +38,7 @@ constexpr int kDecThreads = 128;
 constexpr int kDecWarps = 4;
 constexpr int kDecKeys = 16;      // keys of a tile
 constexpr int kDecStages = 3;
+constexpr int kDecItem = 8;       // an item's fixed cost in tiles
 
 template <int D>
 struct DecCfg {
@@ -82,8 +86,11 @@ __device__ __forceinline__ Seen seen_of(const DecodeParams &p, int b) {
 
 __device__ __forceinline__ int tiles_of(const Seen &x) { return (x.n + kDecKeys - 1) / kDecKeys; }
 
-// Tiles of a CTA's run: at least two for each warp, so that small batches are not spread
-// so thin that joining costs more than reading.
+// Cost of an item of nt tiles, in tiles.
+__device__ __forceinline__ int cost_of(int nt) { return nt > 0 ? nt + kDecItem : 0; }
+
+// Length of a CTA's run: at least two tiles for each warp, so that small batches are not
+// spread so thin that joining costs more than reading.
 __host__ __device__ __forceinline__ int run_of(int total, int ctas) {
   const int r = (total + ctas - 1) / ctas;
   return r < 2 * kDecWarps ? 2 * kDecWarps : r;
@@ -94,7 +101,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
   using C = DecCfg<D>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int sh_sum[kDecWarps + 1];
-  __shared__ int sh_at[2];                 // first sequence of the run, tiles before it
+  __shared__ int sh_at[2];                 // first sequence of the run, cost before it
   __shared__ float sh_m[kDecWarps][16], sh_l[kDecWarps][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr uint32_t FULL = 0xffffffffu;
@@ -104,7 +111,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
   const int R = (p.batch + kDecThreads - 1) / kDecThreads;
   const int bt0 = min(tid * R, p.batch), bt1 = min(bt0 + R, p.batch);
   int mine = 0;
-  for (int b = bt0; b < bt1; ++b) mine += tiles_of(seen_of(p, b)) * items;
+  for (int b = bt0; b < bt1; ++b) mine += cost_of(tiles_of(seen_of(p, b))) * items;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
   if (lo < hi && pre <= lo && lo < pre + mine) {
     int at = pre;
     for (int b = bt0; b < bt1; ++b) {
-      const int t = tiles_of(seen_of(p, b)) * items;
+      const int t = cost_of(tiles_of(seen_of(p, b))) * items;
       if (lo < at + t) {
         sh_at[0] = b;
         sh_at[1] = at;
@@ -138,7 +145,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
     int at = pre;
     for (int b = bt0; b < bt1; ++b) {
       p.before[b] = at;
-      at += tiles_of(seen_of(p, b)) * items;
+      at += cost_of(tiles_of(seen_of(p, b))) * items;
       const long long cap = (long long)p.max_pages * p.page;
       const int len = __ldg(p.seq_lens + b);
       if (len < 0 || len > cap) record_index_error(p.status, (33 * 16) * 256);
@@ -151,39 +158,52 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
   const uint32_t ring = smem_u32(smem) + warp * C::WARP;
   const bool one = p.kp.sb == p.vp.sb && p.kp.sn == p.vp.sn && p.kp.sh == p.vp.sh;
   const int qr = lane >> 2, qc = (lane & 3) * 2;       // fragment row and first column
-  int b = sh_at[0], at = sh_at[1];                     // sequence, tiles before it
+  int b = sh_at[0], at = sh_at[1];                     // sequence, cost before it
   Seen sn = seen_of(p, b);
-  int nt = tiles_of(sn);
-  for (int pos = lo; pos < hi;) {
-    while (nt * items <= pos - at) {                   // next sequence with keys
-      at += nt * items;
+  int nt = tiles_of(sn), cost = cost_of(nt);
+  for (int pos = lo, next; pos < hi; pos = next) {
+    while (cost * items <= pos - at) {                 // next sequence with keys
+      at += cost * items;
       ++b;
       sn = seen_of(p, b);
       nt = tiles_of(sn);
+      cost = cost_of(nt);
     }
-    const int item = (pos - at) / nt;
-    const int t0 = pos - at - item * nt;               // tiles [t0, t1) of the item
-    const int t1 = min(nt, t0 + hi - pos);
+    const int item = (pos - at) / cost;
+    const int begin = at + item * cost;                // the item is [begin, begin + cost)
+    next = min(begin + cost, hi);
+    const int t0 = max(0, pos - begin - kDecItem);     // tiles [t0, t1) of the item
+    const int t1 = next - begin - kDecItem;
+    if (t0 >= t1) continue;                            // its fixed cost alone
     const int hk = item / p.ngrp, h0 = hk * p.G + (item % p.ngrp) * kDecodeRows;
     const int rows = min(kDecodeRows, (hk + 1) * p.G - h0);
     const uint16_t *kb = p.kp.ptr + (int64_t)hk * p.kp.sh, *vb = p.vp.ptr + (int64_t)hk * p.vp.sh;
     const int32_t *tab = p.table + (int64_t)b * p.max_pages;
 
-    // Place in the pages of the lane's row (lanes 0 - 15) of tile t: element offsets, or
-    // -1 for a row behind the last visible key or on a page that is not there.
-    auto place = [&](int t, int64_t &ko, int64_t &vo) {
-      ko = vo = -1;
+    // Place in the pages of the lane's row (lanes 0 - 15) of tile t: page and slot, then
+    // element offsets, or -1 for a row behind the last visible key or on a page that is not
+    // there.
+    struct Place {
+      int id, slot;            // id -2: no key
+    };
+    auto look = [&](int t) {
+      Place x{-2, 0};
       const int v = t * kDecKeys + lane;
       if (lane < kDecKeys && t < t1 && v < sn.n) {
         const int key = v < sn.s ? v : v - sn.s + sn.w0;
-        const int pg = key / p.page, slot = key - pg * p.page;
-        const int id = __ldg(tab + pg);
-        if (id >= 0 && id < p.num_pages) {
-          ko = (int64_t)id * p.kp.sb + (int64_t)slot * p.kp.sn;
-          vo = one ? ko : (int64_t)id * p.vp.sb + (int64_t)slot * p.vp.sn;
-        } else {
-          record_index_error(p.status, (33 * 16 + 1) * 256);
-        }
+        const int pg = key / p.page;
+        x.slot = key - pg * p.page;
+        x.id = max(-1, __ldg(tab + pg));
+      }
+      return x;
+    };
+    auto place = [&](const Place &x, int64_t &ko, int64_t &vo) {
+      ko = vo = -1;
+      if (x.id >= 0 && x.id < p.num_pages) {
+        ko = (int64_t)x.id * p.kp.sb + (int64_t)x.slot * p.kp.sn;
+        vo = one ? ko : (int64_t)x.id * p.vp.sb + (int64_t)x.slot * p.vp.sn;
+      } else if (x.id != -2) {
+        record_index_error(p.status, (33 * 16 + 1) * 256);
       }
     };
     auto issue = [&](int stage, int64_t ko, int64_t vo) {
@@ -203,14 +223,17 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
     int64_t ko, vo;
     uint32_t okm[kDecStages];                          // visible keys of the stages' tiles
     int tl = t0 + warp;                                // next tile to load
+    Place ahead[kDecStages];                           // (page ids of the first tiles together)
+#pragma unroll
+    for (int s = 0; s < kDecStages; ++s) ahead[s] = look(tl + s * kDecWarps);
 #pragma unroll
     for (int s = 0; s < kDecStages - 1; ++s, tl += kDecWarps) {
-      place(tl, ko, vo);
+      place(ahead[s], ko, vo);
       okm[s] = __ballot_sync(FULL, ko >= 0) & 0xffffu;
       if (tl < t1) issue(s, ko, vo);
       cp_async_commit();
     }
-    place(tl, ko, vo);
+    Place nx = ahead[kDecStages - 1];
     uint32_t qa[D / 16][4];
     {
       const uint16_t *q0 = p.q + (int64_t)b * p.q_sb + (int64_t)(h0 + qr) * p.q_sh + qc;
@@ -234,6 +257,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
       // a turn ago; then read the place of the next one.
       {
         const int into = stage == 0 ? kDecStages - 1 : stage - 1;
+        place(nx, ko, vo);
         const uint32_t ok = __ballot_sync(FULL, ko >= 0) & 0xffffu;
 #pragma unroll
         for (int s = 0; s < kDecStages; ++s)
@@ -241,7 +265,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
         if (tl < t1) issue(into, ko, vo);
         cp_async_commit();
         tl += kDecWarps;
-        place(tl, ko, vo);
+        nx = look(tl);
       }
       cp_async_wait_group<kDecStages - 1>();
       __syncwarp();
@@ -341,7 +365,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
-    const int64_t slot = (int64_t)blockIdx.x * 2 + (pos == lo ? 0 : 1);
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (pos == lo ? 0 : 1);   // (lo >= begin: its first)
     for (int i = tid; i < rows * (D / 4); i += kDecThreads) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
       float mx = sh_m[0][r];
@@ -372,23 +396,26 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
       }
     }
     __syncthreads();     // the buffer is read; the next item's loads may overwrite it
-    pos += t1 - t0;
   }
 }
 
 // Joins the partial results of the items that several CTAs share, and writes the empty
-// row of a sequence without visible keys.  One CTA per (sequence, item).
+// row of a sequence without visible keys.  One CTA per (sequence, item): the parts' weights
+// first (all of their log-sum-exps are read at once), then the weighted sum.
 template <int D>
 __global__ void __launch_bounds__(128) paged_decode_join_kernel(const DecodeParams p, int ctas) {
+  __shared__ float wgt[kDecodeRows][kDecodeCtas + 1];
+  __shared__ float inv[kDecodeRows], lse[kDecodeRows];
+  constexpr uint32_t FULL = 0xffffffffu;
   // The partial results are the previous launch's: wait until it has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int items = p.hkv * p.ngrp;
+  const int tid = threadIdx.x, items = p.hkv * p.ngrp;
   const int b = blockIdx.x / items, item = blockIdx.x % items;
   const int hk = item / p.ngrp, h0 = hk * p.G + (item % p.ngrp) * kDecodeRows;
   const int rows = min(kDecodeRows, (hk + 1) * p.G - h0);
-  const int before = p.before[b], nt = (p.before[b + 1] - before) / items, total = p.before[p.batch];
-  if (nt == 0) {
-    for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
+  const int before = p.before[b], cost = (p.before[b + 1] - before) / items, total = p.before[p.batch];
+  if (cost == 0) {
+    for (int i = tid; i < rows * (D / 4); i += 128) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
       *reinterpret_cast<uint2 *>(p.out + (int64_t)b * p.o_sb + (int64_t)(h0 + r) * p.o_sh + c) = make_uint2(0u, 0u);
       if (c == 0) p.lse[(int64_t)b * p.hq + h0 + r] = -INFINITY;
@@ -396,31 +423,52 @@ __global__ void __launch_bounds__(128) paged_decode_join_kernel(const DecodePara
     return;
   }
   const int run = run_of(total, ctas);
-  const int a = before + item * nt, e = a + nt;
-  const int c0 = a / run, c1 = (e - 1) / run;
+  const int a = before + item * cost;                   // the item is [a, a + cost)
+  const int c0 = (a + kDecItem) / run, c1 = (a + cost - 1) / run;
   if (c0 == c1) return;                                 // whole in one CTA
-  for (int i = threadIdx.x; i < rows * (D / 4); i += 128) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float mx = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int x = c0; x <= c1; ++x) {
-      const int64_t slot = (int64_t)x * 2 + ((int64_t)x * run >= a ? 0 : 1);
-      const float z = p.lpart[slot * kDecodeRows + r];
-      const float4 y = *reinterpret_cast<const float4 *>(p.opart + (slot * kDecodeRows + r) * D + c);
-      const float n = fmaxf(mx, z);
-      const float u = n == -INFINITY ? 0.f : n;
-      const float f0 = ex2_approx(mx - u), f1 = ex2_approx(z - u);
-      mx = n;
-      l = fmaf(l, f0, f1);
-      acc[0] = fmaf(acc[0], f0, f1 * y.x);
-      acc[1] = fmaf(acc[1], f0, f1 * y.y);
-      acc[2] = fmaf(acc[2], f0, f1 * y.z);
-      acc[3] = fmaf(acc[3], f0, f1 * y.w);
-    }
+  const int n = c1 - c0 + 1;
+  auto slot = [&](int x) { return (int64_t)(c0 + x) * 2 + ((int64_t)(c0 + x) * run >= a ? 0 : 1); };
+  for (int i = tid; i < rows * n; i += 128) {
+    const int r = i / n, x = i - r * n;
+    wgt[r][x] = p.lpart[slot(x) * kDecodeRows + r];
+  }
+  __syncthreads();
+  for (int r = tid >> 5; r < rows; r += 4) {
+    const int lane = tid & 31;
+    float mx = -INFINITY, l = 0.f;
+    for (int x = lane; x < n; x += 32) mx = fmaxf(mx, wgt[r][x]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
     const float u = mx == -INFINITY ? 0.f : mx;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    for (int x = lane; x < n; x += 32) {
+      const float f = ex2_approx(wgt[r][x] - u);
+      wgt[r][x] = f;
+      l += f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
+    if (lane == 0) {
+      inv[r] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      lse[r] = (u + log2f(l)) * 0.69314718055994530942f;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * (D / 4); i += 128) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int x = 0; x < n; ++x) {
+      const float4 y = *reinterpret_cast<const float4 *>(p.opart + (slot(x) * kDecodeRows + r) * D + c);
+      const float f = wgt[r][x];
+      acc[0] = fmaf(f, y.x, acc[0]);
+      acc[1] = fmaf(f, y.y, acc[1]);
+      acc[2] = fmaf(f, y.z, acc[2]);
+      acc[3] = fmaf(f, y.w, acc[3]);
+    }
+    const float v = inv[r];
     *reinterpret_cast<uint2 *>(p.out + (int64_t)b * p.o_sb + (int64_t)(h0 + r) * p.o_sh + c) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    if (c == 0) p.lse[(int64_t)b * p.hq + h0 + r] = (u + log2f(l)) * 0.69314718055994530942f;
+        make_uint2(pack_bf16x2(acc[0] * v, acc[1] * v), pack_bf16x2(acc[2] * v, acc[3] * v));
+    if (c == 0) p.lse[(int64_t)b * p.hq + h0 + r] = lse[r];
   }
 }
 

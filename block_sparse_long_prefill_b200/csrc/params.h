@@ -267,7 +267,7 @@ struct DecodeParams {
   int page, num_pages, max_pages;
   int window, sink;
   float scale_log2;
-  // Workspace: tiles before each sequence [batch + 1], then the partial results: per CTA
+  // Workspace: work (in tiles) before each sequence [batch + 1], then the partial results: per CTA
   // two slots (its first and its last item) of kDecodeRows rows of D values and their LSE.
   int *before;
   float *opart;            // [ctas, 2, kDecodeRows, D]

@@ -26,6 +26,7 @@
 
 namespace moba {
 
+constexpr int kRopeHeads = 4;   // rows of a lane in flight together (and as many ahead)
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
@@ -122,26 +123,24 @@ __device__ __forceinline__ void mate8(const Place &pl, int interleaved, const ui
   }
 }
 
-// Normalise and rotate one row vector; w, wm: the weights of the lane's and of its
-// partners' columns.
+// Normalise and rotate one row vector: y = (x cw + partner sw) rstd, cw and sw the lane's
+// angles times the weights of its own and of its partners' columns.
 template <int D>
 __device__ __forceinline__ uint4 turn_row(const uint4 &a, bool norm, const Place &pl, int interleaved,
-                                          int base, int v, float eps, const float (&c)[8],
-                                          const float (&s)[8], const float (&w)[8],
-                                          const float (&wm)[8]) {
+                                          int base, int v, float eps, const float (&cw)[8],
+                                          const float (&sw)[8]) {
   float x[8], y[8], u[8];
   unpack8(a, x);
   mate8(pl, interleaved, a, x, y);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = fmaf(y[e], sw[e], x[e] * cw[e]);
   if (norm) {
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
     const float r = rsqrtf(row_sum<D>(ss, base, v) * (1.f / D) + eps);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = fmaf(y[e] * wm[e], s[e], x[e] * w[e] * c[e]) * r;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = fmaf(y[e], s[e], x[e] * c[e]);
+    for (int e = 0; e < 8; ++e) u[e] *= r;
   }
   return pack8(u);
 }
@@ -158,17 +157,55 @@ __device__ __forceinline__ void load_weights(const RopeWeight &wt, const Place &
   }
 }
 
+// Angles times weights.
+__device__ __forceinline__ void load_factors(const Place &pl, const float *cosp, const float *sinp, int rot,
+                                             int pos, const RopeWeight &wt, int v, int lane, float (&cw)[8],
+                                             float (&sw)[8]) {
+  load_angles(pl, cosp, sinp, rot, pos, cw, sw);
+  if (wt.ptr) {
+    float w[8], wm[8];
+    load_weights(wt, pl, v, lane, w, wm);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      cw[e] *= w[e];
+      sw[e] *= wm[e];
+    }
+  }
+}
+
+// A warp's rows: heads h0 .. h0 + nh of one tensor, kRopeHeads at a time, the next ones
+// loaded before these are worked on.
+template <int D, class Out>
+__device__ __forceinline__ void walk_heads(const uint16_t *row, int64_t sh, int nh, bool live, Out out) {
+  uint4 a[kRopeHeads];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i) {
+      a[i] = make_uint4(0, 0, 0, 0);
+      if (live && h + i < nh) a[i] = __ldg(reinterpret_cast<const uint4 *>(row + (int64_t)(h + i) * sh));
+    }
+  };
+  load(0);
+  for (int h = 0; h < nh; h += kRopeHeads) {
+    uint4 c[kRopeHeads];
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i) c[i] = a[i];
+    if (h + kRopeHeads < nh) load(h + kRopeHeads);
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i) out(h + i, c[i]);
+  }
+}
+
 // ------------------------------------------------------------------ forward
 
-constexpr int kRopeHeads = 4;   // heads a warp walks, their rows in flight together
-
+// hpt: heads of a warp's task.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_fwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_fwd_kernel(const RopeParams p, int hpt) {
   constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
   const int lane = threadIdx.x & 31;
   const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
   const bool in = v < LPR;
-  const int cq = (p.hq + kRopeHeads - 1) / kRopeHeads, ck = (p.hkv + kRopeHeads - 1) / kRopeHeads;
+  const int cq = (p.hq + hpt - 1) / hpt, ck = (p.hkv + hpt - 1) / hpt;
   const int groups = (p.N + RPW - 1) / RPW;
   const long long task = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
   const int hc = (int)(task % (cq + ck));
@@ -179,8 +216,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_fwd_kernel(const Ro
   const bool isq = hc < cq;
   const RopeTensor src = isq ? p.q : p.k, dst = isq ? p.qo : p.ko;
   const RopeWeight wt = isq ? p.qw : p.kw;
-  const int h0 = (isq ? hc : hc - cq) * kRopeHeads;
-  const int nh = min(kRopeHeads, (isq ? p.hq : p.hkv) - h0);
+  const int h0 = (isq ? hc : hc - cq) * hpt;
+  const int nh = min(hpt, (isq ? p.hq : p.hkv) - h0);
   bool live = in && n < p.N;
   int pos = n;
   if (live && p.positions) pos = __ldg(p.positions + (int64_t)b * p.N + n);
@@ -190,39 +227,32 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_fwd_kernel(const Ro
   }
   const int vv = in ? v : 0;
   const Place pl = place_of(vv, lane, p.rot, p.interleaved);
-  const uint16_t *row = src.ptr + b * src.sb + (int64_t)n * src.sn + vv * 8;
-  uint16_t *out = dst.ptr + b * dst.sb + (int64_t)n * dst.sn + vv * 8;
-  uint4 a[kRopeHeads];
-#pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i) {
-    a[i] = make_uint4(0, 0, 0, 0);
-    if (live && i < nh) a[i] = __ldg(reinterpret_cast<const uint4 *>(row + (int64_t)(h0 + i) * src.sh));
-  }
-  float c[8], s[8], w[8], wm[8];
-  load_angles(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, c, s);
-  const bool norm = wt.ptr != nullptr;
-  load_weights(wt, pl, vv, lane, w, wm);
-#pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i) {
-    const uint4 o = turn_row<D>(a[i], norm, pl, p.interleaved, base, vv, p.eps, c, s, w, wm);
-    if (live && i < nh) *reinterpret_cast<uint4 *>(out + (int64_t)(h0 + i) * dst.sh) = o;
-  }
+  uint16_t *out = dst.ptr + b * dst.sb + (int64_t)n * dst.sn + vv * 8 + h0 * dst.sh;
+  float cw[8], sw[8];
+  load_factors(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, wt, vv, lane, cw, sw);
+  walk_heads<D>(src.ptr + b * src.sb + (int64_t)n * src.sn + vv * 8 + h0 * src.sh, src.sh, nh, live,
+                [&](int h, const uint4 &a) {
+                  const uint4 o = turn_row<D>(a, wt.ptr != nullptr, pl, p.interleaved, base, vv, p.eps, cw, sw);
+                  if (live && h < nh) *reinterpret_cast<uint4 *>(out + h * dst.sh) = o;
+                });
 }
 
 // ------------------------------------------------------------------ backward
+
+constexpr int kRopeBwdHeads = 8, kRopeBwdRound = 2;   // heads of a task, rows in flight together
 
 // Persistent: a lane's columns are the same in all of its rows, so it sums their weight
 // gradients in registers; the CTA's lanes of equal columns add up in one order and leave
 // one partial row, which qk_norm_rope_dw_kernel sums over the CTAs (no atomics).
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_bwd_kernel(const RopeParams p) {
   constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
   __shared__ float part[kRopeWarps * RPW][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
   const bool in = v < LPR;
   const int vv = in ? v : 0;
-  const int cq = (p.hq + kRopeHeads - 1) / kRopeHeads, ck = (p.hkv + kRopeHeads - 1) / kRopeHeads;
+  const int cq = (p.hq + kRopeBwdHeads - 1) / kRopeBwdHeads, ck = (p.hkv + kRopeBwdHeads - 1) / kRopeBwdHeads;
   const int groups = (p.N + RPW - 1) / RPW;
   const Place pl = place_of(vv, lane, p.rot, p.interleaved);
   for (int side = 0; side < 2; ++side) {
@@ -231,17 +261,17 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
     const RopeWeight wt = isq ? p.qw : p.kw;
     const bool norm = wt.ptr != nullptr;
     const int heads = isq ? p.hq : p.hkv, chunks = isq ? cq : ck;
-    float w[8], wm[8], dw[8];
-    load_weights(wt, pl, vv, lane, w, wm);
+    float w[8], dw[8];
+    load_weight(wt, vv * 8, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[e] = 0.f;
     const long long tasks = (long long)chunks * groups * p.batch;
     for (long long task = (long long)blockIdx.x * kRopeWarps + warp; task < tasks;
          task += (long long)gridDim.x * kRopeWarps) {
-      const int h0 = (int)(task % chunks) * kRopeHeads;
+      const int h0 = (int)(task % chunks) * kRopeBwdHeads;
       const long long tg = task / chunks;
       const int b = (int)(tg / groups), n = (int)(tg % groups) * RPW + sub;
-      const int nh = min(kRopeHeads, heads - h0);
+      const int nh = min(kRopeBwdHeads, heads - h0);
       bool live = in && n < p.N;
       int pos = n;
       if (live && p.positions) pos = __ldg(p.positions + (int64_t)b * p.N + n);
@@ -249,47 +279,60 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
         live = false;
         record_index_error(p.status, (32 * 16 + 2) * 256);
       }
-      const uint16_t *grow = up.ptr + b * up.sb + (int64_t)n * up.sn + vv * 8;
-      const uint16_t *xrow = src.ptr + b * src.sb + (int64_t)n * src.sn + vv * 8;
-      uint16_t *out = dst.ptr + b * dst.sb + (int64_t)n * dst.sn + vv * 8;
-      uint4 ga[kRopeHeads], xa[kRopeHeads];
+      const uint16_t *grow = up.ptr + b * up.sb + (int64_t)n * up.sn + vv * 8 + h0 * up.sh;
+      const uint16_t *xrow = src.ptr + b * src.sb + (int64_t)n * src.sn + vv * 8 + h0 * src.sh;
+      uint16_t *out = dst.ptr + b * dst.sb + (int64_t)n * dst.sn + vv * 8 + h0 * dst.sh;
+      constexpr int R = kRopeBwdRound;
+      uint4 ga[R], xa[R];
+      auto load = [&](int h) {
 #pragma unroll
-      for (int i = 0; i < kRopeHeads; ++i) {
-        ga[i] = xa[i] = make_uint4(0, 0, 0, 0);
-        if (live && i < nh) {
-          ga[i] = __ldg(reinterpret_cast<const uint4 *>(grow + (int64_t)(h0 + i) * up.sh));
-          if (norm) xa[i] = __ldg(reinterpret_cast<const uint4 *>(xrow + (int64_t)(h0 + i) * src.sh));
+        for (int i = 0; i < R; ++i) {
+          ga[i] = xa[i] = make_uint4(0, 0, 0, 0);
+          if (live && h + i < nh) {
+            ga[i] = __ldg(reinterpret_cast<const uint4 *>(grow + (int64_t)(h + i) * up.sh));
+            if (norm) xa[i] = __ldg(reinterpret_cast<const uint4 *>(xrow + (int64_t)(h + i) * src.sh));
+          }
         }
-      }
+      };
+      load(0);
       float c[8], s[8];
       load_angles(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, c, s);
+      for (int h = 0; h < nh; h += R) {
+        uint4 gc[R], xc[R];
 #pragma unroll
-      for (int i = 0; i < kRopeHeads; ++i) {
-        float dy[8], ym[8], g[8], x[8];
-        unpack8(ga[i], dy);
-        mate8(pl, p.interleaved, ga[i], dy, ym);
-        // R^T: the sines turn their sign.
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = fmaf(ym[e], -s[e], dy[e] * c[e]);
-        if (norm) {
-          unpack8(xa[i], x);
-          float ss = 0.f, gx = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = fmaf(x[e], x[e], ss);
-            gx = fmaf(g[e] * w[e], x[e], gx);
-          }
-          ss = row_sum<D>(ss, base, vv);
-          gx = row_sum<D>(gx, base, vv);
-          const float r = rsqrtf(ss * (1.f / D) + p.eps);
-          const float m = gx * (1.f / D) * r * r;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dw[e] = fmaf(g[e] * r, x[e], dw[e]);
-            g[e] = r * fmaf(-m, x[e], g[e] * w[e]);
-          }
+        for (int i = 0; i < R; ++i) {
+          gc[i] = ga[i];
+          xc[i] = xa[i];
         }
-        if (live && i < nh) *reinterpret_cast<uint4 *>(out + (int64_t)(h0 + i) * dst.sh) = pack8(g);
+        if (h + R < nh) load(h + R);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          float dy[8], ym[8], g[8], x[8];
+          unpack8(gc[i], dy);
+          mate8(pl, p.interleaved, gc[i], dy, ym);
+          // R^T: the sines turn their sign.
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] = fmaf(ym[e], -s[e], dy[e] * c[e]);
+          if (norm) {
+            unpack8(xc[i], x);
+            float ss = 0.f, gx = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              ss = fmaf(x[e], x[e], ss);
+              gx = fmaf(g[e] * w[e], x[e], gx);
+            }
+            ss = row_sum<D>(ss, base, vv);
+            gx = row_sum<D>(gx, base, vv);
+            const float r = rsqrtf(ss * (1.f / D) + p.eps);
+            const float m = gx * (1.f / D) * r * r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              dw[e] = fmaf(g[e] * r, x[e], dw[e]);
+              g[e] = r * fmaf(-m, x[e], g[e] * w[e]);
+            }
+          }
+          if (live && h + i < nh) *reinterpret_cast<uint4 *>(out + (int64_t)(h + i) * dst.sh) = pack8(g);
+        }
       }
     }
     if (!norm) continue;   // (uniform over the grid)
@@ -349,17 +392,17 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int batch, int lan
   return mine < batch ? mine : -1;
 }
 
-// Heads of a token in the order queries, keys, values; a warp takes kRopeHeads of one of
-// the three and the tokens of its rows.
+// Heads of a token in the order queries, keys, values; a warp takes hpt of one of the three
+// and the tokens of its rows.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const AppendParams p, int hpt) {
   constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
   const int lane = threadIdx.x & 31;
   const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
   const bool in = v < LPR;
   const int vv = in ? v : 0;
-  const int cq = p.q.ptr ? (p.hq + kRopeHeads - 1) / kRopeHeads : 0;
-  const int ck = (p.hkv + kRopeHeads - 1) / kRopeHeads;
+  const int cq = p.q.ptr ? (p.hq + hpt - 1) / hpt : 0;
+  const int ck = (p.hkv + hpt - 1) / hpt;
   const long long task = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
   const int hc = (int)(task % (cq + 2 * ck));
   const long long t0 = task / (cq + 2 * ck) * RPW;
@@ -368,18 +411,9 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(const AppendPar
   const int which = hc < cq ? 0 : (hc < cq + ck ? 1 : 2);   // q, k, v
   const RopeTensor src = which == 0 ? p.q : (which == 1 ? p.k : p.v);
   const RopeWeight wt = which == 0 ? p.qw : p.kw;
-  const int h0 = (which == 0 ? hc : (which == 1 ? hc - cq : hc - cq - ck)) * kRopeHeads;
-  const int nh = min(kRopeHeads, (which == 0 ? p.hq : p.hkv) - h0);
+  const int h0 = (which == 0 ? hc : (which == 1 ? hc - cq : hc - cq - ck)) * hpt;
+  const int nh = min(hpt, (which == 0 ? p.hq : p.hkv) - h0);
   bool live = in && t < p.T;
-  uint4 a[kRopeHeads];
-  {
-    const uint16_t *row = src.ptr + (int64_t)t * src.sn + vv * 8;
-#pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i) {
-      a[i] = make_uint4(0, 0, 0, 0);
-      if (live && i < nh) a[i] = __ldg(reinterpret_cast<const uint4 *>(row + (int64_t)(h0 + i) * src.sh));
-    }
-  }
   // The token's sequence and position, and its place in the pages.
   int seq = t, pos = 0, pid = 0, slot = 0;
   if (p.cu) seq = sequence_of(p.cu, p.batch, lane, RPW, LPR, (int)t0);
@@ -413,21 +447,20 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(const AppendPar
     osh = dst.sh;
   }
   out += vv * 8 + h0 * osh;
+  const uint16_t *row = src.ptr + (int64_t)t * src.sn + vv * 8 + h0 * src.sh;
   if (which == 2) {
-#pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i)
-      if (live && i < nh) *reinterpret_cast<uint4 *>(out + i * osh) = a[i];
+    walk_heads<D>(row, src.sh, nh, live, [&](int h, const uint4 &a) {
+      if (live && h < nh) *reinterpret_cast<uint4 *>(out + h * osh) = a;
+    });
     return;
   }
   const Place pl = place_of(vv, lane, p.cosp ? p.rot : 0, p.interleaved);
-  float c[8], s[8], w[8], wm[8];
-  load_angles(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, c, s);
-  load_weights(wt, pl, vv, lane, w, wm);
-#pragma unroll
-  for (int i = 0; i < kRopeHeads; ++i) {
-    const uint4 o = turn_row<D>(a[i], wt.ptr != nullptr, pl, p.interleaved, base, vv, p.eps, c, s, w, wm);
-    if (live && i < nh) *reinterpret_cast<uint4 *>(out + i * osh) = o;
-  }
+  float cw[8], sw[8];
+  load_factors(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, wt, vv, lane, cw, sw);
+  walk_heads<D>(row, src.sh, nh, live, [&](int h, const uint4 &a) {
+    const uint4 o = turn_row<D>(a, wt.ptr != nullptr, pl, p.interleaved, base, vv, p.eps, cw, sw);
+    if (live && h < nh) *reinterpret_cast<uint4 *>(out + h * osh) = o;
+  });
 }
 
 // ------------------------------------------------------------------ launch
@@ -436,11 +469,21 @@ static unsigned rope_blocks(long long tasks) {
   return (unsigned)((tasks + kRopeWarps - 1) / kRopeWarps);
 }
 
+// Heads of a task: two rounds of kRopeHeads, so that the angles serve eight rows and one
+// round's loads run while the other is worked on; one round, or one head, where the whole
+// call would not fill the GPU (148 SMs, 24 warps each) otherwise.
+static int rope_heads(long long rows_per_head, int heads) {
+  for (int hpt = 2 * kRopeHeads; hpt > 1; hpt /= 2)
+    if (rows_per_head * ((heads + hpt - 1) / hpt) >= 148 * 24) return hpt;
+  return 1;
+}
+
 template <int D>
 static cudaError_t launch_rope_fwd_d(const RopeParams &p, cudaStream_t st) {
-  const long long chunks = (p.hq + kRopeHeads - 1) / kRopeHeads + (p.hkv + kRopeHeads - 1) / kRopeHeads;
-  const long long groups = (p.N + RowLanes<D>::RPW - 1) / RowLanes<D>::RPW;
-  qk_norm_rope_fwd_kernel<D><<<rope_blocks(chunks * groups * p.batch), kRopeThreads, 0, st>>>(p);
+  const long long groups = (long long)((p.N + RowLanes<D>::RPW - 1) / RowLanes<D>::RPW) * p.batch;
+  const int hpt = rope_heads(groups, p.hq + p.hkv);
+  const long long chunks = (p.hq + hpt - 1) / hpt + (p.hkv + hpt - 1) / hpt;
+  qk_norm_rope_fwd_kernel<D><<<rope_blocks(chunks * groups), kRopeThreads, 0, st>>>(p, hpt);
   return cudaGetLastError();
 }
 
@@ -456,7 +499,7 @@ cudaError_t launch_rope_fwd(const RopeParams &p, int d, cudaStream_t st) {
 // CTAs of the backward, each with one partial row of weight gradients per side.
 int rope_bwd_ctas(int batch, int hq, int hkv, int N, int d) {
   const long long rpw = 32 / (d / 8);
-  const long long chunks = (hq + kRopeHeads - 1) / kRopeHeads + (hkv + kRopeHeads - 1) / kRopeHeads;
+  const long long chunks = (hq + kRopeBwdHeads - 1) / kRopeBwdHeads + (hkv + kRopeBwdHeads - 1) / kRopeBwdHeads;
   const long long blocks = (chunks * ((N + rpw - 1) / rpw) * batch + kRopeWarps - 1) / kRopeWarps;
   return (int)(blocks < kRopeBwdCtas ? blocks : kRopeBwdCtas);
 }
@@ -481,10 +524,11 @@ cudaError_t launch_rope_bwd(const RopeParams &p, int d, int grid, cudaStream_t s
 
 template <int D>
 static cudaError_t launch_append_d(const AppendParams &p, cudaStream_t st) {
-  const long long ck = (p.hkv + kRopeHeads - 1) / kRopeHeads;
-  const long long cq = p.q.ptr ? (p.hq + kRopeHeads - 1) / kRopeHeads : 0;
   const long long groups = (p.T + RowLanes<D>::RPW - 1) / RowLanes<D>::RPW;
-  kv_append_kernel<D><<<rope_blocks((cq + 2 * ck) * groups), kRopeThreads, 0, st>>>(p);
+  const int hpt = rope_heads(groups, (p.q.ptr ? p.hq : 0) + 2 * p.hkv);
+  const long long ck = (p.hkv + hpt - 1) / hpt;
+  const long long cq = p.q.ptr ? (p.hq + hpt - 1) / hpt : 0;
+  kv_append_kernel<D><<<rope_blocks((cq + 2 * ck) * groups), kRopeThreads, 0, st>>>(p, hpt);
   return cudaGetLastError();
 }
 
