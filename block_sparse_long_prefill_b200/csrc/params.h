@@ -201,7 +201,7 @@ inline size_t bwd_workspace_bytes(int batch, int hq, int N, int d, int topk, siz
   return a + align_up(rows * size_t(topk) * size_t(d) * 4, 256);
 }
 
-constexpr int kRopeBwdCtas = 592;  // most CTAs (partial weight-gradient rows) of the norm + rotary backward
+constexpr int kRopeBwdCtas = 296;  // most CTAs (partial weight-gradient rows) of the norm + rotary backward
 
 // Parameters of the per-head norm + rotary kernels (rope.cu).  Rows are (b, head, n);
 // strides in elements.

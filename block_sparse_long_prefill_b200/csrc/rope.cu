@@ -12,8 +12,8 @@
 //
 // The work is one read and one write of every row, so it is HBM-bound.  A lane holds one
 // 16-byte vector (8 columns) of a row, d / 8 lanes a row, so a warp carries 32 / (d / 8)
-// tokens; it walks a run of heads of these tokens with several rows in flight and keeps
-// the angles (and weights) of its columns in registers meanwhile.  In the half layout a
+// tokens; it takes a run of heads of these tokens, all of their rows in flight (cp.async into
+// slots of its own), and keeps the angles times the weights of its columns in registers.  In the half layout a
 // column's partner sits in another lane's vector: four shuffles of packed bf16 pairs fetch
 // it, and the row sums are a butterfly of the same lanes.
 #include <cuda_bf16.h>
@@ -26,7 +26,7 @@
 
 namespace moba {
 
-constexpr int kRopeHeads = 4;   // rows of a lane in flight together (and as many ahead)
+constexpr int kRopeHeads = 8;   // most heads of a warp's task, their rows in flight together
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
@@ -173,35 +173,19 @@ __device__ __forceinline__ void load_factors(const Place &pl, const float *cosp,
   }
 }
 
-// A warp's rows: heads h0 .. h0 + nh of one tensor, kRopeHeads at a time, the next ones
-// loaded before these are worked on.
-template <int D, class Out>
-__device__ __forceinline__ void walk_heads(const uint16_t *row, int64_t sh, int nh, bool live, Out out) {
-  uint4 a[kRopeHeads];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i) {
-      a[i] = make_uint4(0, 0, 0, 0);
-      if (live && h + i < nh) a[i] = __ldg(reinterpret_cast<const uint4 *>(row + (int64_t)(h + i) * sh));
-    }
-  };
-  load(0);
-  for (int h = 0; h < nh; h += kRopeHeads) {
-    uint4 c[kRopeHeads];
-#pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i) c[i] = a[i];
-    if (h + kRopeHeads < nh) load(h + kRopeHeads);
-#pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i) out(h + i, c[i]);
-  }
+// A lane's slots in shared memory: it copies its own vectors there and reads them back, so
+// rows in flight cost no registers and need no barrier.
+__device__ __forceinline__ uint32_t lane_slot(const uint4 *buf, int i) {
+  return smem_u32(buf + i * 32 + (threadIdx.x & 31));
 }
 
 // ------------------------------------------------------------------ forward
 
 // hpt: heads of a warp's task.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_fwd_kernel(const RopeParams p, int hpt) {
+__global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_fwd_kernel(const RopeParams p, int hpt) {
   constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
+  __shared__ uint4 slots[kRopeWarps][kRopeHeads * 32];
   const int lane = threadIdx.x & 31;
   const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
   const bool in = v < LPR;
@@ -228,113 +212,138 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_fwd_kernel(const
   const int vv = in ? v : 0;
   const Place pl = place_of(vv, lane, p.rot, p.interleaved);
   uint16_t *out = dst.ptr + b * dst.sb + (int64_t)n * dst.sn + vv * 8 + h0 * dst.sh;
+  // (A lane without a row of its own reads the tensor's first.)
+  const uint16_t *row = src.ptr + (live ? b * src.sb + (int64_t)n * src.sn + vv * 8 : 0) + h0 * src.sh;
+  uint4 *buf = slots[threadIdx.x >> 5];
+  for (int h = 0; h < nh; ++h) cp_async_16(lane_slot(buf, h), row + h * src.sh);
+  cp_async_commit();
   float cw[8], sw[8];
   load_factors(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, wt, vv, lane, cw, sw);
-  walk_heads<D>(src.ptr + b * src.sb + (int64_t)n * src.sn + vv * 8 + h0 * src.sh, src.sh, nh, live,
-                [&](int h, const uint4 &a) {
-                  const uint4 o = turn_row<D>(a, wt.ptr != nullptr, pl, p.interleaved, base, vv, p.eps, cw, sw);
-                  if (live && h < nh) *reinterpret_cast<uint4 *>(out + h * dst.sh) = o;
-                });
+  cp_async_wait_all();
+#pragma unroll 2
+  for (int h = 0; h < nh; ++h) {
+    const uint4 o = turn_row<D>(buf[h * 32 + lane], wt.ptr != nullptr, pl, p.interleaved, base, vv, p.eps, cw, sw);
+    if (live) *reinterpret_cast<uint4 *>(out + h * dst.sh) = o;
+  }
 }
 
 // ------------------------------------------------------------------ backward
 
-constexpr int kRopeBwdHeads = 8, kRopeBwdRound = 2;   // heads of a task, rows in flight together
+constexpr int kRopeRound = 4;   // heads of a round of the backward
 
 // Persistent: a lane's columns are the same in all of its rows, so it sums their weight
 // gradients in registers; the CTA's lanes of equal columns add up in one order and leave
-// one partial row, which qk_norm_rope_dw_kernel sums over the CTAs (no atomics).
+// one partial row, which qk_norm_rope_dw_kernel sums over the CTAs (no atomics).  A round is
+// four heads of a warp's tokens; the next round's rows are in flight while one is worked on,
+// and two rounds in a row share a token's angles.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_bwd_kernel(const RopeParams p) {
-  constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
+__global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const RopeParams p) {
+  constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW, R = kRopeRound;
+  extern __shared__ __align__(16) unsigned char rope_smem[];   // [warp][buffer][g, x][R][32] vectors
   __shared__ float part[kRopeWarps * RPW][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
   const bool in = v < LPR;
   const int vv = in ? v : 0;
-  const int cq = (p.hq + kRopeBwdHeads - 1) / kRopeBwdHeads, ck = (p.hkv + kRopeBwdHeads - 1) / kRopeBwdHeads;
+  uint4 *ring = reinterpret_cast<uint4 *>(rope_smem) + warp * (2 * 2 * R * 32);
   const int groups = (p.N + RPW - 1) / RPW;
   const Place pl = place_of(vv, lane, p.rot, p.interleaved);
+  const int gw = blockIdx.x * kRopeWarps + warp, nw = gridDim.x * kRopeWarps;
   for (int side = 0; side < 2; ++side) {
     const bool isq = side == 0;
     const RopeTensor src = isq ? p.q : p.k, dst = isq ? p.qo : p.ko, up = isq ? p.gq : p.gk;
     const RopeWeight wt = isq ? p.qw : p.kw;
     const bool norm = wt.ptr != nullptr;
-    const int heads = isq ? p.hq : p.hkv, chunks = isq ? cq : ck;
-    float w[8], dw[8];
+    const int heads = isq ? p.hq : p.hkv, chunks = (heads + R - 1) / R;
+    float w[8], dw[8], c[8], s[8];
     load_weight(wt, vv * 8, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[e] = 0.f;
-    const long long tasks = (long long)chunks * groups * p.batch;
-    for (long long task = (long long)blockIdx.x * kRopeWarps + warp; task < tasks;
-         task += (long long)gridDim.x * kRopeWarps) {
-      const int h0 = (int)(task % chunks) * kRopeBwdHeads;
-      const long long tg = task / chunks;
-      const int b = (int)(tg / groups), n = (int)(tg % groups) * RPW + sub;
-      const int nh = min(kRopeBwdHeads, heads - h0);
-      bool live = in && n < p.N;
-      int pos = n;
-      if (live && p.positions) pos = __ldg(p.positions + (int64_t)b * p.N + n);
-      if (live && (pos < 0 || pos >= p.max_pos)) {
-        live = false;
+    // Rounds in pairs: a warp takes the rounds 2 k, 2 k + 1 for k = gw, gw + nw, ...
+    const long long rounds = (long long)chunks * groups * p.batch;
+    auto after = [&](long long k) { return (k & 1) ? k + 2ll * nw - 1 : k + 1; };
+    struct Round {
+      int b, n, h0, nh, pos;
+      bool live;
+      long long tg;
+    };
+    auto decode = [&](long long k) {
+      Round x;
+      x.tg = k / chunks;
+      x.h0 = (int)(k - x.tg * chunks) * R;
+      x.nh = min(R, heads - x.h0);
+      x.b = (int)(x.tg / groups);
+      x.n = (int)(x.tg - (long long)x.b * groups) * RPW + sub;
+      x.live = in && x.n < p.N;
+      x.pos = x.n;
+      if (x.live && p.positions) x.pos = __ldg(p.positions + (int64_t)x.b * p.N + x.n);
+      if (x.live && (x.pos < 0 || x.pos >= p.max_pos)) {
+        x.live = false;
         record_index_error(p.status, (32 * 16 + 2) * 256);
       }
-      const uint16_t *grow = up.ptr + b * up.sb + (int64_t)n * up.sn + vv * 8 + h0 * up.sh;
-      const uint16_t *xrow = src.ptr + b * src.sb + (int64_t)n * src.sn + vv * 8 + h0 * src.sh;
-      uint16_t *out = dst.ptr + b * dst.sb + (int64_t)n * dst.sn + vv * 8 + h0 * dst.sh;
-      constexpr int R = kRopeBwdRound;
-      uint4 ga[R], xa[R];
-      auto load = [&](int h) {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          ga[i] = xa[i] = make_uint4(0, 0, 0, 0);
-          if (live && h + i < nh) {
-            ga[i] = __ldg(reinterpret_cast<const uint4 *>(grow + (int64_t)(h + i) * up.sh));
-            if (norm) xa[i] = __ldg(reinterpret_cast<const uint4 *>(xrow + (int64_t)(h + i) * src.sh));
-          }
-        }
-      };
-      load(0);
-      float c[8], s[8];
-      load_angles(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, c, s);
-      for (int h = 0; h < nh; h += R) {
-        uint4 gc[R], xc[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          gc[i] = ga[i];
-          xc[i] = xa[i];
-        }
-        if (h + R < nh) load(h + R);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          float dy[8], ym[8], g[8], x[8];
-          unpack8(gc[i], dy);
-          mate8(pl, p.interleaved, gc[i], dy, ym);
-          // R^T: the sines turn their sign.
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = fmaf(ym[e], -s[e], dy[e] * c[e]);
-          if (norm) {
-            unpack8(xc[i], x);
-            float ss = 0.f, gx = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              ss = fmaf(x[e], x[e], ss);
-              gx = fmaf(g[e] * w[e], x[e], gx);
-            }
-            ss = row_sum<D>(ss, base, vv);
-            gx = row_sum<D>(gx, base, vv);
-            const float r = rsqrtf(ss * (1.f / D) + p.eps);
-            const float m = gx * (1.f / D) * r * r;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              dw[e] = fmaf(g[e] * r, x[e], dw[e]);
-              g[e] = r * fmaf(-m, x[e], g[e] * w[e]);
-            }
-          }
-          if (live && h + i < nh) *reinterpret_cast<uint4 *>(out + (int64_t)(h + i) * dst.sh) = pack8(g);
-        }
+      return x;
+    };
+    auto issue = [&](const Round &x, int buf) {
+      const uint16_t *g = up.ptr + (x.live ? x.b * up.sb + (int64_t)x.n * up.sn + vv * 8 : 0) + x.h0 * up.sh;
+      const uint16_t *r = src.ptr + (x.live ? x.b * src.sb + (int64_t)x.n * src.sn + vv * 8 : 0) + x.h0 * src.sh;
+      uint4 *to = ring + buf * (2 * R * 32);
+      for (int i = 0; i < x.nh; ++i) {
+        cp_async_16_zfill(lane_slot(to, i), g + i * up.sh, x.live);
+        if (norm) cp_async_16_zfill(lane_slot(to, R + i), r + i * src.sh, x.live);
       }
+    };
+    long long k = 2ll * gw, tg = -1;
+    Round cur{};
+    if (k < rounds) {
+      cur = decode(k);
+      issue(cur, 0);
     }
+    cp_async_commit();
+    for (int buf = 0; k < rounds; buf ^= 1) {
+      const long long kn = after(k);
+      Round nx{};
+      if (kn < rounds) {
+        nx = decode(kn);
+        issue(nx, buf ^ 1);
+      }
+      cp_async_commit();
+      if (cur.tg != tg) load_angles(pl, p.cosp, p.sinp, p.rot, cur.live ? cur.pos : 0, c, s);
+      tg = cur.tg;
+      cp_async_wait_group<1>();
+      uint16_t *out = dst.ptr + cur.b * dst.sb + (int64_t)cur.n * dst.sn + vv * 8 + cur.h0 * dst.sh;
+      const uint4 *from = ring + buf * (2 * R * 32) + lane;
+      for (int i = 0; i < cur.nh; ++i) {
+        const uint4 ga = from[i * 32];
+        float dy[8], ym[8], g[8], x[8];
+        unpack8(ga, dy);
+        mate8(pl, p.interleaved, ga, dy, ym);
+        // R^T: the sines turn their sign.
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = fmaf(ym[e], -s[e], dy[e] * c[e]);
+        if (norm) {
+          unpack8(from[(R + i) * 32], x);
+          float ss = 0.f, gx = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            ss = fmaf(x[e], x[e], ss);
+            gx = fmaf(g[e] * w[e], x[e], gx);
+          }
+          ss = row_sum<D>(ss, base, vv);
+          gx = row_sum<D>(gx, base, vv);
+          const float r = rsqrtf(ss * (1.f / D) + p.eps);
+          const float m = gx * (1.f / D) * r * r;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            dw[e] = fmaf(g[e] * r, x[e], dw[e]);
+            g[e] = r * fmaf(-m, x[e], g[e] * w[e]);
+          }
+        }
+        if (cur.live) *reinterpret_cast<uint4 *>(out + i * dst.sh) = pack8(g);
+      }
+      k = kn;
+      cur = nx;
+    }
+    cp_async_wait_all();
     if (!norm) continue;   // (uniform over the grid)
     __syncthreads();
     if (in) {
@@ -395,8 +404,9 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int batch, int lan
 // Heads of a token in the order queries, keys, values; a warp takes hpt of one of the three
 // and the tokens of its rows.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const AppendParams p, int hpt) {
+__global__ void __launch_bounds__(kRopeThreads, 4) kv_append_kernel(const AppendParams p, int hpt) {
   constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
+  __shared__ uint4 slots[kRopeWarps][kRopeHeads * 32];
   const int lane = threadIdx.x & 31;
   const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
   const bool in = v < LPR;
@@ -414,6 +424,12 @@ __global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const Append
   const int h0 = (which == 0 ? hc : (which == 1 ? hc - cq : hc - cq - ck)) * hpt;
   const int nh = min(hpt, (which == 0 ? p.hq : p.hkv) - h0);
   bool live = in && t < p.T;
+  {
+    // (A lane without a token of its own reads the tensor's first.)
+    const uint16_t *row = src.ptr + (live ? (int64_t)t * src.sn + vv * 8 : 0) + h0 * src.sh;
+    for (int h = 0; h < nh; ++h) cp_async_16(lane_slot(slots[threadIdx.x >> 5], h), row + h * src.sh);
+    cp_async_commit();
+  }
   // The token's sequence and position, and its place in the pages.
   int seq = t, pos = 0, pid = 0, slot = 0;
   if (p.cu) seq = sequence_of(p.cu, p.batch, lane, RPW, LPR, (int)t0);
@@ -447,20 +463,22 @@ __global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const Append
     osh = dst.sh;
   }
   out += vv * 8 + h0 * osh;
-  const uint16_t *row = src.ptr + (int64_t)t * src.sn + vv * 8 + h0 * src.sh;
+  const uint4 *buf = slots[threadIdx.x >> 5];
   if (which == 2) {
-    walk_heads<D>(row, src.sh, nh, live, [&](int h, const uint4 &a) {
-      if (live && h < nh) *reinterpret_cast<uint4 *>(out + h * osh) = a;
-    });
+    cp_async_wait_all();
+    for (int h = 0; h < nh; ++h)
+      if (live) *reinterpret_cast<uint4 *>(out + h * osh) = buf[h * 32 + lane];
     return;
   }
   const Place pl = place_of(vv, lane, p.cosp ? p.rot : 0, p.interleaved);
   float cw[8], sw[8];
   load_factors(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, wt, vv, lane, cw, sw);
-  walk_heads<D>(row, src.sh, nh, live, [&](int h, const uint4 &a) {
-    const uint4 o = turn_row<D>(a, wt.ptr != nullptr, pl, p.interleaved, base, vv, p.eps, cw, sw);
-    if (live && h < nh) *reinterpret_cast<uint4 *>(out + h * osh) = o;
-  });
+  cp_async_wait_all();
+#pragma unroll 2
+  for (int h = 0; h < nh; ++h) {
+    const uint4 o = turn_row<D>(buf[h * 32 + lane], wt.ptr != nullptr, pl, p.interleaved, base, vv, p.eps, cw, sw);
+    if (live) *reinterpret_cast<uint4 *>(out + h * osh) = o;
+  }
 }
 
 // ------------------------------------------------------------------ launch
@@ -469,12 +487,11 @@ static unsigned rope_blocks(long long tasks) {
   return (unsigned)((tasks + kRopeWarps - 1) / kRopeWarps);
 }
 
-// Heads of a task: two rounds of kRopeHeads, so that the angles serve eight rows and one
-// round's loads run while the other is worked on; one round, or one head, where the whole
-// call would not fill the GPU (148 SMs, 24 warps each) otherwise.
+// Heads of a task: kRopeHeads, so that the angles serve as many rows; fewer where the whole
+// call would not fill the GPU (148 SMs, 32 warps each) otherwise.
 static int rope_heads(long long rows_per_head, int heads) {
-  for (int hpt = 2 * kRopeHeads; hpt > 1; hpt /= 2)
-    if (rows_per_head * ((heads + hpt - 1) / hpt) >= 148 * 24) return hpt;
+  for (int hpt = kRopeHeads; hpt > 1; hpt /= 2)
+    if (rows_per_head * ((heads + hpt - 1) / hpt) >= 148 * 32) return hpt;
   return 1;
 }
 
@@ -499,15 +516,18 @@ cudaError_t launch_rope_fwd(const RopeParams &p, int d, cudaStream_t st) {
 // CTAs of the backward, each with one partial row of weight gradients per side.
 int rope_bwd_ctas(int batch, int hq, int hkv, int N, int d) {
   const long long rpw = 32 / (d / 8);
-  const long long chunks = (hq + kRopeBwdHeads - 1) / kRopeBwdHeads + (hkv + kRopeBwdHeads - 1) / kRopeBwdHeads;
+  const long long chunks = (hq > hkv ? hq : hkv) / (2 * kRopeRound) + 1;   // pairs of rounds of the larger side
   const long long blocks = (chunks * ((N + rpw - 1) / rpw) * batch + kRopeWarps - 1) / kRopeWarps;
   return (int)(blocks < kRopeBwdCtas ? blocks : kRopeBwdCtas);
 }
 
 template <int D>
 static cudaError_t launch_rope_bwd_d(const RopeParams &p, int grid, cudaStream_t st) {
-  qk_norm_rope_bwd_kernel<D><<<grid, kRopeThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  constexpr int smem = kRopeWarps * 2 * 2 * kRopeRound * 32 * 16;
+  cudaError_t e = cudaFuncSetAttribute(qk_norm_rope_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  qk_norm_rope_bwd_kernel<D><<<grid, kRopeThreads, smem, st>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess || (!p.dqw && !p.dkw)) return e;
   qk_norm_rope_dw_kernel<D><<<dim3((D + 31) / 32, 2), 256, 0, st>>>(p, grid);
   return cudaGetLastError();
