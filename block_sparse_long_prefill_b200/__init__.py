@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -122,11 +123,12 @@ def _check(fn: str, rc: int) -> None:
 
 def _t(x: torch.Tensor) -> MobaTensor:
     """[b, h, n, d] tensor with a contiguous last dimension -> moba_tensor."""
-    if x.dim() != 4:
+    st = x.stride()
+    if len(st) != 4:
         raise ValueError("expected a [batch, heads, N, d] tensor")
-    if x.stride(3) != 1:
+    if st[3] != 1:
         raise ValueError("the head dimension must be contiguous")
-    return MobaTensor(x.data_ptr(), x.stride(0), x.stride(1), x.stride(2))
+    return MobaTensor(x.data_ptr(), st[0], st[1], st[2])
 
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -160,9 +162,9 @@ def _device(fn: str, *specs):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:   # (the handle without a torch.cuda.Stream around it: 0.1 us, not 4)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 _HERE_ALREADY = contextlib.nullcontext()
@@ -322,6 +324,7 @@ def swa_attn_fwd_chunk(q, k, v, window: int, scale: float = 0.0, out=None, lse=N
     return out, lse
 
 
+@functools.lru_cache(maxsize=256)
 def swa_bwd_workspace_size(batch, hq, hkv, N, d, window, sink=0) -> int:
     out = ctypes.c_size_t(0)
     _check("swa_bwd_workspace_size",
@@ -438,11 +441,12 @@ def _tokens(x):
     """[tokens, heads, d] -> moba_tensor with sn between tokens and sh between heads."""
     if x is None:
         return MobaTensor(None, 0, 0, 0)
-    if x.dim() != 3:
+    st = x.stride()
+    if len(st) != 3:
         raise ValueError("expected a [tokens, heads, d] tensor")
-    if x.stride(2) != 1:
+    if st[2] != 1:
         raise ValueError("the head dimension must be contiguous")
-    return MobaTensor(x.data_ptr(), 0, x.stride(1), x.stride(0))
+    return MobaTensor(x.data_ptr(), 0, st[1], st[0])
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos=None, sin=None,
@@ -483,11 +487,22 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def paged_decode_workspace_size(batch, hq, hkv, d) -> int:
     out = ctypes.c_size_t(0)
     _check("paged_decode_workspace_size",
            _lib.paged_decode_workspace_size(batch, hq, hkv, d, ctypes.byref(out)))
     return out.value
+
+
+def _rows(x):
+    """[sequences, heads, d] -> moba_tensor with sb between sequences and sh between heads."""
+    st = x.stride()
+    if len(st) != 3:
+        raise ValueError("expected a [batch, heads, d] tensor")
+    if st[2] != 1:
+        raise ValueError("the head dimension must be contiguous")
+    return MobaTensor(x.data_ptr(), st[0], st[1], 0)
 
 
 def paged_decode_attn(q, k_pages, v_pages, page_table, seq_lens, window: int = 0, sink: int = 0,
@@ -512,14 +527,9 @@ def paged_decode_attn(q, k_pages, v_pages, page_table, seq_lens, window: int = 0
         if workspace is None:
             workspace = _empty((paged_decode_workspace_size(batch, hq, hkv, d),), torch.uint8, dev)
 
-        def rows(x):
-            if x.stride(2) != 1:
-                raise ValueError("the head dimension must be contiguous")
-            return MobaTensor(x.data_ptr(), x.stride(0), x.stride(1), 0)
-
-        _check(fn, _lib.paged_decode_attn(rows(q), _t(k_pages), _t(v_pages), page_table.data_ptr(),
+        _check(fn, _lib.paged_decode_attn(_rows(q), _t(k_pages), _t(v_pages), page_table.data_ptr(),
                                           seq_lens.data_ptr(), batch, hq, hkv, d, page, pages,
-                                          page_table.shape[1], window, sink, float(scale), rows(out),
+                                          page_table.shape[1], window, sink, float(scale), _rows(out),
                                           lse.data_ptr(), workspace.data_ptr(),
                                           workspace.numel() * workspace.element_size(), _stream(None)))
     return out, lse
