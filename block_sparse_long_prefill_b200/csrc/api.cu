@@ -40,7 +40,7 @@ cudaError_t launch_rope_fwd(const RopeParams &p, int d, cudaStream_t st);
 cudaError_t launch_rope_bwd(const RopeParams &p, int d, int grid, cudaStream_t st);
 int rope_bwd_ctas(int batch, int hq, int hkv, int N, int d);
 cudaError_t launch_append(const AppendParams &p, int d, cudaStream_t st);
-cudaError_t launch_decode(const DecodeParams &p, int d, int ctas, cudaStream_t st);
+cudaError_t launch_decode(const DecodeParams &p, int d, int nsm, cudaStream_t st);
 
 namespace {
 
@@ -929,8 +929,7 @@ int paged_decode_attn(moba_tensor q, moba_tensor k_pages, moba_tensor v_pages,
   p.before = reinterpret_cast<int *>(ws);
   p.opart = reinterpret_cast<float *>(ws + off_o);
   p.lpart = reinterpret_cast<float *>(ws + off_l);
-  const int ctas = 2 * nsm < kDecodeCtas ? 2 * nsm : kDecodeCtas;
-  return launch_status(launch_decode(p, d, ctas, static_cast<cudaStream_t>(stream)));
+  return launch_status(launch_decode(p, d, nsm, static_cast<cudaStream_t>(stream)));
 }
 
 int moba_device_status(void) {

@@ -8,7 +8,7 @@
 // Every visible key and value is read once and used for the G query heads of its KV head,
 // so the work is HBM-bound (4 G flops a byte at most).  The keys of a (sequence, KV head,
 // group of up to 16 query heads) -- an item -- are cut into tiles of 16, and the work of
-// the batch is dealt out in equal runs to a grid of two CTAs per SM, whatever the
+// the batch is dealt out in equal runs to a grid of two or three CTAs per SM, whatever the
 // sequences' lengths: a run may end inside an item, which then has partial results
 // (normalised rows and their log-sum-exp) that a second, small kernel joins.  An item counts
 // as its tiles and kDecItem more, about what filling the pipeline and joining the warps
@@ -49,6 +49,7 @@ struct DecCfg {
   static constexpr int WARP = kDecStages * STAGE;     // a warp's ring
   static constexpr int OROW = D + 4;                  // floats of a row of the joining buffer
   static constexpr int SMEM = kDecWarps * WARP;
+  static constexpr int PER_SM = D == 128 ? 2 : 3;     // resident CTAs (shared memory, registers)
   static_assert(kDecWarps * 16 * OROW * 4 <= SMEM, "the joining buffer lies over the rings");
 };
 
@@ -97,7 +98,7 @@ __host__ __device__ __forceinline__ int run_of(int total, int ctas) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D>::PER_SM) paged_decode_kernel(const DecodeParams p) {
   using C = DecCfg<D>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int sh_sum[kDecWarps + 1];
@@ -402,10 +403,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Deco
 // Joins the partial results of the items that several CTAs share, and writes the empty
 // row of a sequence without visible keys.  One CTA per (sequence, item): the parts' weights
 // first (all of their log-sum-exps are read at once), then the weighted sum.
+// Its warps take a row each and, where there are fewer rows than warps, a share of the parts.
+constexpr int kJoinWarps = 16;
 template <int D>
-__global__ void __launch_bounds__(128) paged_decode_join_kernel(const DecodeParams p, int ctas) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_decode_join_kernel(const DecodeParams p, int ctas) {
   __shared__ float wgt[kDecodeRows][kDecodeCtas + 1];
   __shared__ float inv[kDecodeRows], lse[kDecodeRows];
+  __shared__ float4 sum[kJoinWarps][D / 4];
   constexpr uint32_t FULL = 0xffffffffu;
   // The partial results are the previous launch's: wait until it has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(128) paged_decode_join_kernel(const DecodePara
   const int rows = min(kDecodeRows, (hk + 1) * p.G - h0);
   const int before = p.before[b], cost = (p.before[b + 1] - before) / items, total = p.before[p.batch];
   if (cost == 0) {
-    for (int i = tid; i < rows * (D / 4); i += 128) {
+    for (int i = tid; i < rows * (D / 4); i += 32 * kJoinWarps) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
       *reinterpret_cast<uint2 *>(p.out + (int64_t)b * p.o_sb + (int64_t)(h0 + r) * p.o_sh + c) = make_uint2(0u, 0u);
       if (c == 0) p.lse[(int64_t)b * p.hq + h0 + r] = -INFINITY;
@@ -428,12 +432,12 @@ __global__ void __launch_bounds__(128) paged_decode_join_kernel(const DecodePara
   if (c0 == c1) return;                                 // whole in one CTA
   const int n = c1 - c0 + 1;
   auto slot = [&](int x) { return (int64_t)(c0 + x) * 2 + ((int64_t)(c0 + x) * run >= a ? 0 : 1); };
-  for (int i = tid; i < rows * n; i += 128) {
+  for (int i = tid; i < rows * n; i += 32 * kJoinWarps) {
     const int r = i / n, x = i - r * n;
     wgt[r][x] = p.lpart[slot(x) * kDecodeRows + r];
   }
   __syncthreads();
-  for (int r = tid >> 5; r < rows; r += 4) {
+  for (int r = tid >> 5; r < rows; r += kJoinWarps) {
     const int lane = tid & 31;
     float mx = -INFINITY, l = 0.f;
     for (int x = lane; x < n; x += 32) mx = fmaxf(mx, wgt[r][x]);
@@ -453,29 +457,43 @@ __global__ void __launch_bounds__(128) paged_decode_join_kernel(const DecodePara
     }
   }
   __syncthreads();
-  for (int i = tid; i < rows * (D / 4); i += 128) {
-    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int warp = tid >> 5, lane = tid & 31;
+  const int shares = kJoinWarps / rows, r = warp % rows, share = warp / rows;
+  if (share < shares && lane < D / 4) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int x = 0; x < n; ++x) {
-      const float4 y = *reinterpret_cast<const float4 *>(p.opart + (slot(x) * kDecodeRows + r) * D + c);
+    for (int x = share; x < n; x += shares) {
+      const float4 y = *reinterpret_cast<const float4 *>(p.opart + (slot(x) * kDecodeRows + r) * D + lane * 4);
       const float f = wgt[r][x];
-      acc[0] = fmaf(f, y.x, acc[0]);
-      acc[1] = fmaf(f, y.y, acc[1]);
-      acc[2] = fmaf(f, y.z, acc[2]);
-      acc[3] = fmaf(f, y.w, acc[3]);
+      acc.x = fmaf(f, y.x, acc.x);
+      acc.y = fmaf(f, y.y, acc.y);
+      acc.z = fmaf(f, y.z, acc.z);
+      acc.w = fmaf(f, y.w, acc.w);
+    }
+    sum[warp][lane] = acc;
+  }
+  __syncthreads();
+  if (share == 0 && lane < D / 4) {
+    float4 acc = sum[warp][lane];
+    for (int x = 1; x < shares; ++x) {
+      const float4 y = sum[warp + x * rows][lane];
+      acc.x += y.x;
+      acc.y += y.y;
+      acc.z += y.z;
+      acc.w += y.w;
     }
     const float v = inv[r];
-    *reinterpret_cast<uint2 *>(p.out + (int64_t)b * p.o_sb + (int64_t)(h0 + r) * p.o_sh + c) =
-        make_uint2(pack_bf16x2(acc[0] * v, acc[1] * v), pack_bf16x2(acc[2] * v, acc[3] * v));
-    if (c == 0) p.lse[(int64_t)b * p.hq + h0 + r] = lse[r];
+    *reinterpret_cast<uint2 *>(p.out + (int64_t)b * p.o_sb + (int64_t)(h0 + r) * p.o_sh + lane * 4) =
+        make_uint2(pack_bf16x2(acc.x * v, acc.y * v), pack_bf16x2(acc.z * v, acc.w * v));
+    if (lane == 0) p.lse[(int64_t)b * p.hq + h0 + r] = lse[r];
   }
 }
 
 // ------------------------------------------------------------------ launch
 
 template <int D>
-static cudaError_t launch_decode_d(const DecodeParams &p, int ctas, cudaStream_t st) {
+static cudaError_t launch_decode_d(const DecodeParams &p, int nsm, cudaStream_t st) {
+  const int ctas = min(DecCfg<D>::PER_SM * nsm, kDecodeCtas);
   cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        DecCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
@@ -484,7 +502,7 @@ static cudaError_t launch_decode_d(const DecodeParams &p, int ctas, cudaStream_t
   // The join may be set up while the main kernel runs; it waits for its completion.
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.batch * p.hkv * p.ngrp));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -494,11 +512,11 @@ static cudaError_t launch_decode_d(const DecodeParams &p, int ctas, cudaStream_t
   return cudaLaunchKernelEx(&cfg, paged_decode_join_kernel<D>, p, ctas);
 }
 
-cudaError_t launch_decode(const DecodeParams &p, int d, int ctas, cudaStream_t st) {
+cudaError_t launch_decode(const DecodeParams &p, int d, int nsm, cudaStream_t st) {
   switch (d) {
-    case 64: return launch_decode_d<64>(p, ctas, st);
-    case 80: return launch_decode_d<80>(p, ctas, st);
-    case 128: return launch_decode_d<128>(p, ctas, st);
+    case 64: return launch_decode_d<64>(p, nsm, st);
+    case 80: return launch_decode_d<80>(p, nsm, st);
+    case 128: return launch_decode_d<128>(p, nsm, st);
   }
   return cudaErrorInvalidValue;
 }

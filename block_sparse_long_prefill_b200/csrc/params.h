@@ -251,7 +251,7 @@ struct AppendParams {
 
 // Parameters of the paged decode (decode.cu).  One query token per sequence, at the last
 // of its seq_lens[b] positions.
-constexpr int kDecodeCtas = 296;      // most CTAs of the main kernel (two per SM)
+constexpr int kDecodeCtas = 444;      // most CTAs of the main kernel (three per SM)
 constexpr int kDecodeRows = 16;       // query heads of one KV head a CTA takes together
 struct DecodeParams {
   int *status;
