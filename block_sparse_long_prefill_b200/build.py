@@ -10,8 +10,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoba.so")
 SOURCES = ["api.cu", "select.cu", "gate.cu", "attn.cu", "merge.cu", "noalloc.cu", "bwd.cu",
-           "swa_bwd.cu", "rope.cu", "decode.cu"]
-HEADERS = ["common.cuh", "params.h", "lists.cuh", "rows.cuh"]
+           "swa_fwd.cu", "swa_bwd.cu", "rope.cu", "decode.cu"]
+HEADERS = ["common.cuh", "params.h", "lists.cuh", "rows.cuh", "swa_tile.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

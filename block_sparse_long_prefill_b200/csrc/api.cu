@@ -35,6 +35,7 @@ cudaError_t launch_merge(const MergeParams &p, cudaStream_t st);
 int query_major_units(int batch, int hq, int hkv, int block, int is_moba, int row_begin,
                       int row_end);
 cudaError_t launch_bwd(const CUtensorMap *maps, const BwdParams &p, int nsm, cudaStream_t st);
+cudaError_t launch_swa_fwd(const CUtensorMap *maps, const AttnParams &p, int nsm, cudaStream_t st);
 cudaError_t launch_swa_bwd(const CUtensorMap *maps, const SwaBwdParams &p, int nsm, cudaStream_t st);
 cudaError_t launch_rope_fwd(const RopeParams &p, int d, cudaStream_t st);
 cudaError_t launch_rope_bwd(const RopeParams &p, int d, int grid, cudaStream_t st);
@@ -613,11 +614,16 @@ int swa_sink_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, in
   p.is_moba = 0;
   p.row_begin = 0;
   p.row_end = N;
-  p.ntiles = query_major_units(batch, hq, hkv, 0, 0, 0, N);
   p.npast = 0;
+  if (p.sink > 0) {
+    const long long tiles = (long long)batch * hq * ((N + kTileRows - 1) / kTileRows);
+    if (tiles >= (1ll << 30)) return MOBA_ERR_SHAPE;
+    p.ntiles = (int)tiles;
+    return launch_status(launch_swa_fwd(maps, p, nsm, static_cast<cudaStream_t>(stream)));
+  }
+  p.ntiles = query_major_units(batch, hq, hkv, 0, 0, 0, N);
   const int grid = p.ntiles < nsm ? p.ntiles : nsm;
-  return launch_status(launch_attn(maps, p, p.sink > 0 ? kSinkBand : kQueryMajor, grid,
-                                   static_cast<cudaStream_t>(stream)));
+  return launch_status(launch_attn(maps, p, kQueryMajor, grid, static_cast<cudaStream_t>(stream)));
 }
 
 int swa_attn_fwd_chunk(moba_tensor q, moba_tensor k, moba_tensor v, int batch, int hq, int hkv,

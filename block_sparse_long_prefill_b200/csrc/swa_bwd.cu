@@ -47,109 +47,9 @@
 #include "common.cuh"
 #include "params.h"
 #include "rows.cuh"
+#include "swa_tile.cuh"
 
 namespace moba {
-
-constexpr int kSwaBwdThreads = 384;
-
-// A 128-row tile of D columns: a 64-column region with 128-byte swizzle, then columns
-// [64, 128) the same way (D = 128) or [64, 80) with 32-byte swizzle (D = 80).
-template <int D>
-struct SwaTile {
-  static constexpr int R0 = 128 * 128;
-  static constexpr int R1 = D == 128 ? 128 * 128 : (D == 80 ? 128 * 32 : 0);
-  static constexpr int TILE = R0 + R1;
-  static constexpr uint32_t BYTES = 128u * D * 2u;
-  static_assert(BYTES == (uint32_t)TILE, "a tile is packed");
-};
-
-// High descriptor words: 128-byte swizzle (8-row groups 1024 bytes apart) and the 32-byte
-// swizzle of the D = 80 tail (256 bytes apart).
-constexpr uint32_t kHi128 = desc_hi(1024, kSwizzle128), kHi32 = desc_hi(256, kSwizzle32);
-
-// D[tmem, D columns] (+)= A[tmem] B over the tile's rows [64 half, 64 half + 64): four steps
-// of 16 rows, A's in consecutive groups of 8 columns.  fresh: the first step overwrites.
-template <int D>
-__device__ __forceinline__ void swa_acc(uint32_t d, uint32_t a, uint32_t tile, int half, bool fresh) {
-  const uint32_t b = desc_lo(tile, D == 128 ? SwaTile<D>::R0 : 16) + half * 512;
-  const uint32_t b1 = desc_lo(tile + SwaTile<D>::R0, 16) + half * 128;
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    const uint32_t acc = (kk == 0 && fresh) ? 0u : 1u;
-    umma_ts_w(d, a + kk * 8, b + kk * 128, kHi128, idesc_bf16(128, D == 128 ? 128 : 64, 0, 1), acc);
-    if (D == 80) umma_ts_w(d + 64, a + kk * 8, b1 + kk * 32, kHi32, idesc_bf16(128, 16, 0, 1), acc);
-  }
-}
-
-// S (NB columns) = A B^T over the D columns; A and B K-major tiles, B's NB rows from row0 on.
-// extra_a, extra_b: blocks of 16 more columns (32-byte rows, 32-byte swizzle), or 0.
-template <int D, int NB>
-__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int row0, uint32_t extra_a = 0,
-                                           uint32_t extra_b = 0) {
-  constexpr uint32_t id = idesc_bf16(128, NB, 0, 0);
-  const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16) + row0 * 8;
-#pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    const uint32_t acc = ks > 0 ? 1u : 0u;
-    if (D == 80 && ks == 4)
-      umma_ss_w(d, al + SwaTile<D>::R0 / 16, kHi32, desc_lo(b + SwaTile<D>::R0, 16) + row0 * 2, kHi32, id, acc);
-    else
-      umma_ss_w(d, al + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128,
-                bl + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128, id, acc);
-  }
-  if (extra_a) umma_ss_w(d, desc_lo(extra_a, 16), kHi32, desc_lo(extra_b, 16) + row0 * 2, kHi32, id, 1u);
-}
-
-template <int D>
-__device__ __forceinline__ void swa_load_tile(unsigned char *dst, const CUtensorMap *m, const CUtensorMap *m1,
-                                              uint64_t *bar, int row, int h, int b) {
-  tma_load_4d(dst, m, bar, 0, row, h, b);
-  if (D != 64) tma_load_4d(dst + SwaTile<D>::R0, m1, bar, 64, row, h, b);
-}
-
-// Bulk copy (16-byte aligned on both sides).
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-// After an abort: waits (with the limit) until the last loads of a ring have landed.
-__device__ __forceinline__ void drain_ring(uint64_t *full, uint32_t cnt, uint32_t stages, const int *status) {
-  for (uint32_t u = cnt > stages ? cnt - stages : 0; u < cnt; ++u) {
-    const unsigned long long t0 = global_timer_ns();
-    while (!mbar_try_wait(&full[u % stages], (u / stages) & 1) && global_timer_ns() - t0 < wait_limit_ns(status)) {}
-  }
-}
-
-// Packed fp32 pairs, each lane rounded as the scalar instruction would.
-__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b, float c0, float c1) {
-  const float2 d = __ffma2_rn(make_float2(a0, a1), make_float2(b, b), make_float2(c0, c1));
-  d0 = d.x;
-  d1 = d.y;
-}
-__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
-  const float2 d = __fmul2_rn(make_float2(a0, a1), make_float2(b0, b1));
-  d0 = d.x;
-  d1 = d.y;
-}
-// d = p * (v + c) on pairs.
-__device__ __forceinline__ void addmul2(float &d0, float &d1, float v0, float v1, float c0, float c1,
-                                        float p0, float p1) {
-  const float2 d = __fmul2_rn(__fadd2_rn(make_float2(v0, v1), make_float2(c0, c1)), make_float2(p0, p1));
-  d0 = d.x;
-  d1 = d.y;
-}
-
-// The n lowest of 32 bits (n below 0: none, above 32: all).
-__device__ __forceinline__ uint32_t first_bits(int n) {
-  return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
-}
-// Bits e and e + 1 of b as the halves of a packed pair.
-__device__ __forceinline__ uint32_t pair_mask(uint32_t b, int e) {
-  return ((b >> e) & 1u ? 0x0000FFFFu : 0u) | ((b >> (e + 1)) & 1u ? 0xFFFF0000u : 0u);
-}
 
 // The statistics of a query tile as 16 more columns of its Q and dO (dK / dV kernel): there
 // a thread holds a key and every query of the tile, so -lse / scale and -D would have to come
@@ -301,31 +201,8 @@ __device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps) {
   fence_barrier_init();
 }
 
-// The end of an issuing warp: everything it issued completes (within the wait limit)
-// before TMEM is released.
-__device__ __forceinline__ void swa_issued(uint64_t *done, const int *status) {
-  if (elect_one()) {
-    umma_commit(done);
-    const unsigned long long t0 = global_timer_ns();
-    while (!mbar_try_wait(done, 0) && global_timer_ns() - t0 < wait_limit_ns(status)) {}
-  }
-}
-
-// 16 columns of accumulators, scaled, as bf16 to a row.
-__device__ __forceinline__ void store16(uint16_t *dst, const uint32_t (&o)[16], float sc) {
-#pragma unroll
-  for (int e = 0; e < 16; e += 8) {
-    uint4 x;
-    x.x = pack_bf16x2(__uint_as_float(o[e]) * sc, __uint_as_float(o[e + 1]) * sc);
-    x.y = pack_bf16x2(__uint_as_float(o[e + 2]) * sc, __uint_as_float(o[e + 3]) * sc);
-    x.z = pack_bf16x2(__uint_as_float(o[e + 4]) * sc, __uint_as_float(o[e + 5]) * sc);
-    x.w = pack_bf16x2(__uint_as_float(o[e + 6]) * sc, __uint_as_float(o[e + 7]) * sc);
-    *reinterpret_cast<uint4 *>(dst + e) = x;
-  }
-}
-
 template <int D>
-__global__ void __launch_bounds__(kSwaBwdThreads, 1)
+__global__ void __launch_bounds__(kSwaThreads, 1)
 swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                   const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG1,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
@@ -627,7 +504,7 @@ struct SwaDkvCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kSwaBwdThreads, 1)
+__global__ void __launch_bounds__(kSwaThreads, 1)
 swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                     const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG1,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
@@ -647,7 +524,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
   if (tid == 0) swa_init_bars(bar, 4);
   // The blocks of ones: columns 0 - 2 (lse) and 3 - 5 (D).
-  for (int r = tid; r < 2 * 128; r += kSwaBwdThreads) {
+  for (int r = tid; r < 2 * 128; r += kSwaThreads) {
     unsigned char *blk = sbase + C::ONE_OFF + (r >> 7) * kSwaExtra;
     const uint4 ones = r < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u);
     *reinterpret_cast<uint4 *>(blk + extra_offset(r & 127, 0)) = ones;
@@ -934,14 +811,14 @@ static cudaError_t launch_swa_bwd_d(const CUtensorMap *m, const SwaBwdParams &p,
   e = cudaFuncSetAttribute(swa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaDqCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.batch * p.hq * p.nt;
-  swa_bwd_dq_kernel<D><<<(int)(items < nsm ? items : nsm), kSwaBwdThreads, SwaDqCfg<D>::SMEM, st>>>(
+  swa_bwd_dq_kernel<D><<<(int)(items < nsm ? items : nsm), kSwaThreads, SwaDqCfg<D>::SMEM, st>>>(
       m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   e = cudaFuncSetAttribute(swa_bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaDkvCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.batch * p.hkv * (p.nst * p.nseg + p.nt);
-  swa_bwd_dkdv_kernel<D><<<(int)(units < nsm ? units : nsm), kSwaBwdThreads, SwaDkvCfg<D>::SMEM, st>>>(
+  swa_bwd_dkdv_kernel<D><<<(int)(units < nsm ? units : nsm), kSwaThreads, SwaDkvCfg<D>::SMEM, st>>>(
       m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 

@@ -1,0 +1,415 @@
+// swa_fwd.cu -- sliding-window attention with sinks, forward, on sm_100a tensor cores.
+//
+// [SWA] = "SWA + MoE: 어텐션과 희소 전문가", Bit-Axon architecture page (§"어텐션 공식",
+//         §"슬라이딩 윈도우 마스크").
+//
+// Query row i at position p = q_off + i attends the keys j <= p with p - j < window or
+// j < sink: out = softmax(scale q K^T) V over them, in one pass with a running maximum and
+// sum.  A work item is a 128-row tile of one head; it walks its chunks of 128 keys, the
+// sinks' before the band, then the band's.
+//
+// A softmax is a chain (scores to registers, maximum, exponentials, write-back, product),
+// and a chain that must end before its next scores can be issued leaves both the tensor core
+// and the exponential unit idle.  So a chunk is split by keys between two streams of four
+// warps, 64 keys each, that share nothing but the query tile: a stream has its own running
+// maximum and sum, its own accumulator, and two buffers for its scores, so that the next
+// scores are there when it has written its probabilities.  The two partial results of a row
+// are joined when the item is read out, behind the first chunk of the next item.  (The two
+// streams of attn.cu are query tiles of 128 keys; their scores and accumulators fill TMEM
+// with one buffer each.)
+//
+// Per 128 x 128 keys 16384 exponentials at 16 a cycle are 1024 cycles; the products are 827
+// cycles at D = 80 and 1291 at D = 128 (64-key products are fed by shared memory: 48 cycles
+// instead of 32).
+//   warp 0      TMA: K and V
+//   warp 1      issues S = Q K^T (TMEM owner)
+//   warp 2      issues O += P V
+//   warp 3      TMA: Q
+//   warps 4-11  streams 0 and 1; a thread owns one TMEM lane, a row
+// Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "params.h"
+#include "swa_tile.cuh"
+
+namespace moba {
+
+constexpr float kSwaRaise = 8.f;   // the running maximum is raised when it grows by 2^8
+
+// Work item u: one 128-row query tile and its chunks: ns of sinks from key 0, then the
+// band's from chunk c0.
+struct SwaItem {
+  int b, h, hk, qt, ns, c0, nc;
+};
+
+__device__ __forceinline__ SwaItem swa_item(const AttnParams &p, int u) {
+  const int nt = (p.N + kTileRows - 1) / kTileRows;
+  SwaItem w;
+  w.qt = nt - 1 - u % nt;                        // later (longer) walks first
+  const int bh = u / nt;
+  w.b = bh / p.hq;
+  w.h = bh % p.hq;
+  w.hk = w.h / p.G;
+  const int first = p.q_off + w.qt * kTileRows;  // position of the first row, of the last:
+  const int last = p.q_off + min(p.N, (w.qt + 1) * kTileRows) - 1;
+  w.c0 = max(0, first - p.window + 1) / kTileKeys;
+  w.ns = min((p.sink + kTileKeys - 1) / kTileKeys, w.c0);
+  w.nc = w.ns + last / kTileKeys - w.c0 + 1;
+  return w;
+}
+
+__device__ __forceinline__ int swa_key(const SwaItem &w, int m) {
+  return (m < w.ns ? m : w.c0 + m - w.ns) * kTileKeys;
+}
+
+template <int D>
+struct SwaFwdCfg {
+  static constexpr int QS = 2;                                 // Q stages
+  static constexpr int NK = D == 128 ? 2 : 4;                  // K and V stages
+  static constexpr int NV = D == 128 ? 2 : 4;
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = QS * SwaTile<D>::TILE;
+  static constexpr int V_OFF = K_OFF + NK * SwaTile<D>::TILE;
+  static constexpr int ML_OFF = V_OFF + NV * SwaTile<D>::TILE; // [item parity][stream][128] (m, l)
+  static constexpr int BAR_OFF = ML_OFF + 2 * 2 * 128 * 8;
+  static constexpr int SMEM = BAR_OFF + 1024 + 1024;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  // TMEM: stream x's scores at 128 x and 128 x + 64 (P is written back over them), its
+  // accumulator.
+  static constexpr uint32_t O = 256;
+  static_assert(O + 2 * D <= 512, "TMEM columns");
+};
+
+struct SwaFwdBars {
+  uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // per stream, of even and odd chunks
+  uint64_t o_full, o_empty, ml_full;
+  uint64_t mma_done[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kSwaThreads, 1)
+swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
+               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV1,
+               const AttnParams p) {
+  using C = SwaFwdCfg<D>;
+  using T = SwaTile<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char *sbase = smem_raw + (base - raw);
+  SwaFwdBars &bar = *reinterpret_cast<SwaFwdBars *>(sbase + C::BAR_OFF);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int site0 = (42 * 16 + (D == 64 ? 0 : (D == 80 ? 1 : 2))) * 256;
+  constexpr uint32_t FULL = 0xffffffffu;
+  const int nitems = p.ntiles;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.q_full[s], 1);
+      mbar_init(&bar.q_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bar.k_full[s], 1);
+      mbar_init(&bar.k_empty[s], 1);
+      mbar_init(&bar.v_full[s], 1);
+      mbar_init(&bar.v_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x)
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&bar.s_full[x][s], 1);
+        mbar_init(&bar.p_full[x][s], 4);     // (a warp arrives once)
+        mbar_init(&bar.pv_done[x][s], 1);
+      }
+    mbar_init(&bar.o_full, 1);
+    mbar_init(&bar.o_empty, 8);
+    mbar_init(&bar.ml_full, 8);
+    mbar_init(&bar.mma_done[0], 1);
+    mbar_init(&bar.mma_done[1], 1);
+    bar.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(FULL, bar.tmem_base, 0);   // (uniform)
+  volatile int *abort = &bar.abort;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K and V
+    uint32_t cnt = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
+      const SwaItem w = swa_item(p, u);
+      for (int m = 0; m < w.nc; ++m, ++cnt) {
+        const uint32_t ks = cnt % C::NK, vs = cnt % C::NV;
+        if (!(ok = mbar_wait_warp(&bar.k_empty[ks], ((cnt / C::NK) & 1) ^ 1, abort, p.status, site0 + 1))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar.k_full[ks], T::BYTES);
+          swa_load_tile<D>(sbase + C::K_OFF + ks * T::TILE, &tmK, &tmK1, &bar.k_full[ks], swa_key(w, m), w.hk, w.b);
+        }
+        __syncwarp();
+        if (!(ok = mbar_wait_warp(&bar.v_empty[vs], ((cnt / C::NV) & 1) ^ 1, abort, p.status, site0 + 1))) {
+          ++cnt;       // (K was issued)
+          break;
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar.v_full[vs], T::BYTES);
+          swa_load_tile<D>(sbase + C::V_OFF + vs * T::TILE, &tmV, &tmV1, &bar.v_full[vs], swa_key(w, m), w.hk, w.b);
+        }
+        __syncwarp();
+      }
+    }
+    if (*abort) {
+      drain_ring(bar.k_full, cnt, C::NK, p.status);
+      drain_ring(bar.v_full, cnt, C::NV, p.status);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ Q
+    uint32_t cnt = 0;
+    for (int u = blockIdx.x; u < nitems; u += gridDim.x, ++cnt) {
+      const SwaItem w = swa_item(p, u);
+      const uint32_t st = cnt % C::QS;
+      if (!mbar_wait_warp(&bar.q_empty[st], ((cnt / C::QS) & 1) ^ 1, abort, p.status, site0 + 2)) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&bar.q_full[st], T::BYTES);
+        swa_load_tile<D>(sbase + C::Q_OFF + st * T::TILE, &tmQ, &tmQ1, &bar.q_full[st], w.qt * kTileRows, w.h, w.b);
+      }
+      __syncwarp();
+    }
+    if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S
+    // Of each chunk and stream, once the buffer's last probabilities have been consumed.
+    uint32_t step = 0, qn = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++qn) {
+      const SwaItem w = swa_item(p, u);
+      const uint32_t qs = qn % C::QS, qt = base + C::Q_OFF + qs * T::TILE;
+      if (!(ok = mbar_wait_warp(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
+      for (int m = 0; ok && m < w.nc; ++m, ++step) {
+        const uint32_t ks = step % C::NK, kt = base + C::K_OFF + ks * T::TILE, sl = step & 1;
+        if (!(ok = mbar_wait_warp(&bar.k_full[ks], (step / C::NK) & 1, abort, p.status, site0 + 4))) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!(ok = mbar_wait_warp(&bar.pv_done[x][sl], ((step >> 1) & 1) ^ 1, abort, p.status, site0 + 5))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            swa_scores<D, 64>(tmem + 128 * x + 64 * sl, qt, kt, 64 * x);
+            umma_commit(&bar.s_full[x][sl]);
+            if (x == 1) {
+              umma_commit(&bar.k_empty[ks]);
+              if (m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    swa_issued(&bar.mma_done[0], p.status);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O += P V
+    uint32_t step = 0, an = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++an) {
+      const SwaItem w = swa_item(p, u);
+      for (int m = 0; ok && m < w.nc; ++m, ++step) {
+        const uint32_t vs = step % C::NV, vt = base + C::V_OFF + vs * T::TILE, sl = step & 1;
+        if (!(ok = mbar_wait_warp(&bar.v_full[vs], (step / C::NV) & 1, abort, p.status, site0 + 6))) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!(ok = mbar_wait_warp(&bar.p_full[x][sl], (step >> 1) & 1, abort, p.status, site0 + 7))) break;
+          if (m == 0 && x == 0 && !(ok = mbar_wait_warp(&bar.o_empty, (an & 1) ^ 1, abort, p.status, site0 + 8))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            swa_acc<D>(tmem + C::O + D * x, tmem + 128 * x + 64 * sl, vt, x, m == 0);
+            umma_commit(&bar.pv_done[x][sl]);
+            if (x == 1) {
+              umma_commit(&bar.v_empty[vs]);
+              if (m == w.nc - 1) umma_commit(&bar.o_full);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    swa_issued(&bar.mma_done[1], p.status);
+  } else {
+    // ------------------------------------------------------------ softmax, and O out
+    const int q4 = warp & 3, x = (warp - 4) >> 2;
+    const int r = 32 * q4 + lane;                   // row == TMEM lane
+    const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+    const uint32_t tO = tmem + lane_off + C::O;
+    float2 *ml = reinterpret_cast<float2 *>(sbase + C::ML_OFF);
+    const float sl2 = p.scale_log2;
+    uint32_t sc = 0, an = 0;                        // chunks, items read out
+    bool ok = true, pend = false, live = false;
+    uint16_t *dst = nullptr;                        // the last item's row, its place in lse
+    float *ldst = nullptr;
+    auto read_out = [&]() {
+      if (!mbar_wait_warp(&bar.ml_full, an & 1, abort, p.status, site0 + 9)) return false;
+      if (!mbar_wait_warp(&bar.o_full, an & 1, abort, p.status, site0 + 10)) return false;
+      tc_fence_after();
+      const float2 a = ml[(an & 1) * 256 + r], b = ml[(an & 1) * 256 + 128 + r];
+      ++an;
+      const float mx = fmaxf(a.x, b.x), mu = mx == -INFINITY ? 0.f : mx;
+      const float fa = ex2_approx(a.x - mu), fb = ex2_approx(b.x - mu);
+      const float l = fmaf(fa, a.y, fb * b.y), inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      const float wa = fa * inv, wb = fb * inv;
+      constexpr int CUT = D == 80 ? 48 : D / 2;     // columns that stream 0 writes
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        if ((c < CUT) != (x == 0)) continue;
+        uint32_t u[16], v[16];
+        tmem_ld16(tO + c, u);
+        tmem_ld16(tO + D + c, v);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            u[e] = __float_as_uint(fmaf(wa, __uint_as_float(u[e]), wb * __uint_as_float(v[e])));
+          store16(dst + c, u, 1.f);                 // one whole 32-byte sector of the row
+        }
+      }
+      if (live && x == 0) *ldst = (mu + log2f(l)) * 0.69314718055994530942f;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.o_empty);
+      return true;
+    };
+    uint32_t in = 0;                                // items
+    for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++in) {
+      const SwaItem w = swa_item(p, u);
+      const int i0 = p.q_off + w.qt * kTileRows, pos = i0 + r;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int m = 0; m < w.nc; ++m, ++sc) {
+        const uint32_t sl = sc & 1;
+        if (!(ok = mbar_wait_warp(&bar.s_full[x][sl], (sc >> 1) & 1, abort, p.status, site0 + 11))) break;
+        tc_fence_after();
+        const int key0 = swa_key(w, m) + 64 * x;
+        const bool full = key0 + 63 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 64 <= p.sink);
+        const uint32_t tS = tmem + lane_off + 128 * x + 64 * sl;
+        uint32_t sv[64];
+        float *s = reinterpret_cast<float *>(sv);
+        tmem_ld64(tS, sv);
+        tmem_wait_ld();
+        if (!full) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            const uint32_t b = first_bits(pos + 1 - key0 - c) &
+                               (~first_bits(pos + 1 - p.window - key0 - c) | first_bits(p.sink - key0 - c));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((b >> e) & 1u)) s[c + e] = -INFINITY;
+          }
+        }
+        float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int e = 4; e < 64; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], s[e]);
+        const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2);
+        const bool raise = m_new > m_run + kSwaRaise;        // (from -inf too)
+        if (__any_sync(FULL, raise)) {
+          const float alpha = raise && m_run != -INFINITY ? ex2_approx(m_run - m_new) : 1.f;
+          if (raise) {
+            l_run *= alpha;
+            m_run = m_new;
+          }
+          // O holds the item's chunks before this one once the last product is done.
+          if (__any_sync(FULL, alpha != 1.f)) {
+            if (!(ok = mbar_wait_warp(&bar.pv_done[x][sl ^ 1], ((sc - 1) >> 1) & 1, abort, p.status, site0 + 12))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + D * x + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(tO + D * x + c, o);
+            }
+          }
+        }
+        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t pp[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            fma2(x0, x1, s[c + e], s[c + e + 1], sl2, -mu, -mu);
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            add2(ls[e & 2], ls[(e & 2) + 1], x0, x1);
+            pp[e / 2] = pack_bf16x2(x0, x1);
+          }
+          tmem_st16(tS + c / 2, pp);
+        }
+        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[x][sl]);
+        if (pend) {
+          pend = false;
+          if (!(ok = read_out())) break;
+        }
+      }
+      if (!ok) break;
+      ml[(in & 1) * 256 + 128 * x + r] = make_float2(m_run, l_run);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.ml_full);
+      const int i = w.qt * kTileRows + r;
+      live = i < p.N;
+      dst = p.out + (int64_t)w.b * p.o_sb + (int64_t)w.h * p.o_sh + (int64_t)i * p.o_sn;
+      ldst = p.lse + ((int64_t)w.b * p.hq + w.h) * p.N + i;
+      pend = true;
+    }
+    if (ok && pend) read_out();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ launch
+
+template <int D>
+static cudaError_t launch_swa_fwd_d(const CUtensorMap *m, const AttnParams &p, int nsm, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(swa_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaFwdCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  swa_fwd_kernel<D><<<p.ntiles < nsm ? p.ntiles : nsm, kSwaThreads, SwaFwdCfg<D>::SMEM, st>>>(
+      m[0], m[1], m[2], m[3], m[4], m[5], p);
+  return cudaGetLastError();
+}
+
+// maps: Q, K, V, each with its column tail (D != 64).
+cudaError_t launch_swa_fwd(const CUtensorMap *maps, const AttnParams &p, int nsm, cudaStream_t st) {
+  switch (p.d) {
+    case 64: return launch_swa_fwd_d<64>(maps, p, nsm, st);
+    case 80: return launch_swa_fwd_d<80>(maps, p, nsm, st);
+    case 128: return launch_swa_fwd_d<128>(maps, p, nsm, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace moba

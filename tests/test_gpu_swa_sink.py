@@ -77,9 +77,9 @@ def test_forward_without_sinks_is_the_band():
     a, la = moba.swa_attn_fwd(q, k, v, 200)
     b, lb = moba.swa_attn_fwd(q, k, v, 200, sink=0)
     assert torch.equal(a, b) and torch.equal(la, lb)
-    # Sinks inside every row's window change nothing that is seen.
-    c, lc = moba.swa_attn_fwd(q[:, :, :150], k[:, :, :150], v[:, :, :150], 200, sink=9)
-    assert torch.equal(a[:, :, :150], c) and torch.equal(la[:, :, :150], lc)
+    # Sinks inside every row's window change nothing that is seen (the sums run in another
+    # order: within the bounds, not to the bit).
+    _fwd(1, 4, 2, 150, 150, 128, 200, 9)
 
 
 @pytest.mark.parametrize("d", [64, 80, 128])
