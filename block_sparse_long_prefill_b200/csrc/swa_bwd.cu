@@ -33,7 +33,7 @@
 //   warp 1      issues S and dP (TMEM owner)
 //   warp 2      issues the accumulating products
 //   warp 3      TMA: Q with dO (and the row statistics)
-//   warps 4-11  elementwise groups 0 and 1; a thread owns one TMEM lane
+//   warps 4-19  elementwise groups 0 - 3 of 32 columns each; a thread owns one TMEM lane
 // Issue blocks until the tensor core has room, and a wait costs 85 cycles even when its
 // phase is complete, so one warp that issues everything leaves the tensor core idle during
 // its waits; two overlap theirs.  Every role runs as a whole warp: a lane that polls alone
@@ -50,6 +50,8 @@
 #include "swa_tile.cuh"
 
 namespace moba {
+
+constexpr int kSwaBwdThreads = 640;
 
 // The statistics of a query tile as 16 more columns of its Q and dO (dK / dV kernel): there
 // a thread holds a key and every query of the tile, so -lse / scale and -D would have to come
@@ -192,7 +194,7 @@ __device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps) {
     mbar_init(&bar.ds_full[x][0], warps);
     mbar_init(&bar.ds_full[x][1], warps);
     mbar_init(&bar.acc_full[x], 1);
-    mbar_init(&bar.acc_empty[x], 8);
+    mbar_init(&bar.acc_empty[x], 16);
   }
   for (int x = 0; x < 3; ++x) mbar_init(&bar.slot_empty[x], 1);
   mbar_init(&bar.mma_done[0], 1);
@@ -202,7 +204,7 @@ __device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSwaThreads, 1)
+__global__ void __launch_bounds__(kSwaBwdThreads, 1)
 swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                   const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG1,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
@@ -220,7 +222,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   constexpr uint32_t FULL = 0xffffffffu;
   const int nitems = p.batch * p.hq * p.nt;
 
-  if (tid == 0) swa_init_bars(bar, 8);
+  if (tid == 0) swa_init_bars(bar, 16);
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmG);
@@ -332,12 +334,12 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     swa_issued(&bar.mma_done[1], p.status);
   } else {
     // ------------------------------------------------------------ dS, and dQ out
-    // Group grp takes the columns [64 grp, 64 grp + 64) of S and dP.  An item's dQ is read
+    // Group grp takes the columns [32 grp, 32 grp + 32) of S and dP.  An item's dQ is read
     // out behind the first chunk of the next item, when its last product is long done.
     const int q4 = warp & 3, grp = (warp - 4) >> 2;
     const int r = 32 * q4 + lane;                   // row == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    const uint32_t tP = tmem + lane_off + C::P0 + 64 * grp;
+    const uint32_t tS = tmem + lane_off + 32 * grp, tP = tS + C::P0;
     const float sl2 = p.scale_log2;
     uint32_t sc = 0, an = 0;
     bool ok = true;
@@ -348,10 +350,9 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       ++an;
       tc_fence_after();
       // A lane's 16 columns are one whole 32-byte sector of its row.
-      constexpr int CUT = D == 80 ? 48 : D / 2;     // columns of group 0
 #pragma unroll
       for (int c = 0; c < D; c += 16) {
-        if ((c < CUT) != (grp == 0)) continue;
+        if ((c / 16 & 3) != grp) continue;
         uint32_t o[16];
         tmem_ld16(tmem + lane_off + C::ACC + c, o);
         tmem_wait_ld();
@@ -370,38 +371,32 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       for (int m = 0; m < w.nc; ++m, ++sc) {
         if (!(ok = mbar_wait_warp(&bar.s_full[0], sc & 1, abort, p.status, site0 + 8))) break;
         tc_fence_after();
-        const int key0 = swa_dq_key(w, m) + 64 * grp;
-        const bool full = key0 + 63 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 64 <= p.sink);
-        const uint32_t tS = tmem + lane_off + 64 * grp, tD = tmem + lane_off + C::DS0 + 64 * (sc & 1) + 32 * grp;
-        uint32_t sv[64], pv[64];
-        tmem_ld64(tS, sv);
-        tmem_ld64(tP, pv);
+        const int key0 = swa_dq_key(w, m) + 32 * grp;
+        const bool full = key0 + 31 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 32 <= p.sink);
+        uint32_t sv[32], pv[32];
+        tmem_ld32(tS, sv);
+        tmem_ld32(tP, pv);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_empty[0]);
         // The dS slot's last product is done (it was issued a step ago).
         if (!(ok = mbar_wait_warp(&bar.slot_empty[sc & 1], ((sc >> 1) & 1) ^ 1, abort, p.status, site0 + 11))) break;
+        uint32_t ds[16];
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t ds[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x0, x1, d0, d1;
-            fma2(x0, x1, __uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1]), sl2, nl, nl);
-            addmul2(d0, d1, __uint_as_float(pv[c + e]), __uint_as_float(pv[c + e + 1]), nd, nd, ex2_approx(x0),
-                    ex2_approx(x1));
-            ds[e / 2] = pack_bf16x2(d0, d1);
-          }
-          if (!full) {
-            // Keys that the row does not see: zero halves of the packed pairs.
-            const uint32_t b = first_bits(i + 1 - key0 - c) &
-                               (~first_bits(i + 1 - p.window - key0 - c) | first_bits(p.sink - key0 - c));
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) ds[e / 2] &= pair_mask(b, e);
-          }
-          tmem_st16(tD + c / 2, ds);
+        for (int e = 0; e < 32; e += 2) {
+          float x0, x1, d0, d1;
+          fma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, nl, nl);
+          addmul2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), nd, nd, ex2_approx(x0), ex2_approx(x1));
+          ds[e / 2] = pack_bf16x2(d0, d1);
         }
+        if (!full) {
+          // Keys that the row does not see: zero halves of the packed pairs.
+          const uint32_t b = first_bits(i + 1 - key0) & (~first_bits(i + 1 - p.window - key0) | first_bits(p.sink - key0));
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) ds[e / 2] &= pair_mask(b, e);
+        }
+        tmem_st16(tmem + lane_off + C::DS0 + 64 * (sc & 1) + 16 * grp, ds);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -504,7 +499,7 @@ struct SwaDkvCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kSwaThreads, 1)
+__global__ void __launch_bounds__(kSwaBwdThreads, 1)
 swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                     const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmG1,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
@@ -522,9 +517,9 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   constexpr uint32_t FULL = 0xffffffffu;
   const int nunits = swa_dkv_units(p);
 
-  if (tid == 0) swa_init_bars(bar, 4);
+  if (tid == 0) swa_init_bars(bar, 8);
   // The blocks of ones: columns 0 - 2 (lse) and 3 - 5 (D).
-  for (int r = tid; r < 2 * 128; r += kSwaThreads) {
+  for (int r = tid; r < 2 * 128; r += kSwaBwdThreads) {
     unsigned char *blk = sbase + C::ONE_OFF + (r >> 7) * kSwaExtra;
     const uint4 ones = r < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u);
     *reinterpret_cast<uint4 *>(blk + extra_offset(r & 127, 0)) = ones;
@@ -648,9 +643,9 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           tc_fence_after();
           if (elect_one()) {
             const uint32_t qp = base + C::Q_OFF + st * T::TILE, gp = base + C::DO_OFF + st * T::TILE;
-            const uint32_t tS = tmem + M::s_at(h);   // P^T, then dS^T
-            swa_acc<D>(tV, tS, gp, x, x == 0 && t == w.t0);
-            swa_acc<D>(tK, tS + 32, qp, x, x == 0 && t == w.t0);
+            const uint32_t tS = tmem + M::s_at(h);   // of 32 queries: P^T, then dS^T
+            swa_acc<D, 16>(tV, tS, gp, x, x == 0 && t == w.t0);
+            swa_acc<D, 16>(tK, tS + 16, qp, x, x == 0 && t == w.t0);
             umma_commit(&bar.slot_empty[h % M::S]);
             if (x == 1) {
               umma_commit(&bar.q_empty[st]);
@@ -668,7 +663,8 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int r = 32 * q4 + lane;                   // key of the tile == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
     using M = typename C::M;
-    const uint32_t tP = tmem + lane_off + M::P0 + 64 * grp;
+    const int x = grp >> 1, sub = 32 * (grp & 1);   // half of the tile, its first column there
+    const uint32_t tP = tmem + lane_off + M::P0 + 64 * x + sub;
     const uint32_t tK = tmem + lane_off + M::ACC, tV = tK + D;
     const float sl2 = p.scale_log2;
     uint32_t sc = 0, an = 0;
@@ -679,57 +675,54 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       const int key0 = w.kt * kTileKeys, key = key0 + r;
       int qt = w.first + w.t0 % w.len;
       for (int t = w.t0; t < w.t1; ++t, ++sc) {
-        if (!(ok = mbar_wait_warp(&bar.s_full[grp], sc & 1, abort, p.status, site0 + 8))) break;
+        if (!(ok = mbar_wait_warp(&bar.s_full[x], sc & 1, abort, p.status, site0 + 8))) break;
         tc_fence_after();
-        const int i0 = qt * kTileRows + 64 * grp;   // row of the group's first column
-        const bool full = key0 + kTileKeys - 1 <= i0 && (i0 + 63 - key0 < p.window || key0 + kTileKeys <= p.sink);
+        const int i0 = qt * kTileRows + 64 * x + sub;   // row of the group's first column
+        const bool full = key0 + kTileKeys - 1 <= i0 && (i0 + 31 - key0 < p.window || key0 + kTileKeys <= p.sink);
         if (++qt == w.first + w.len) qt = w.first;
-        const uint32_t tS = tmem + lane_off + M::s_at(2 * sc + grp);
-        uint32_t sv[64], pv[64];
-        tmem_ld64(tS, sv);
-        tmem_ld64(tP, pv);
+        const uint32_t tS = tmem + lane_off + M::s_at(2 * sc + x);
+        uint32_t sv[32], pv[32];
+        tmem_ld32(tS + sub, sv);
+        tmem_ld32(tP, pv);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_empty[grp]);
+        if (lane == 0) mbar_arrive(&bar.p_empty[x]);
+        uint32_t pp[16], dd[16];
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t pp[16], dd[16];
+        for (int e = 0; e < 32; e += 2) {
+          float x0, x1, d0, d1;
+          mul2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), sl2, sl2);
+          x0 = ex2_approx(x0);
+          x1 = ex2_approx(x1);
+          mul2(d0, d1, __uint_as_float(pv[e]), __uint_as_float(pv[e + 1]), x0, x1);
+          pp[e / 2] = pack_bf16x2(x0, x1);
+          dd[e / 2] = pack_bf16x2(d0, d1);
+        }
+        if (!full) {
+          // Rows that do not see the key: zero halves of the packed pairs.
+          const uint32_t b = ~first_bits(key - i0) & (first_bits(key + p.window - i0) | (key < p.sink ? 0xFFFFFFFFu : 0u));
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float x0, x1, d0, d1;
-            mul2(x0, x1, __uint_as_float(sv[c + e]), __uint_as_float(sv[c + e + 1]), sl2, sl2);
-            x0 = ex2_approx(x0);
-            x1 = ex2_approx(x1);
-            mul2(d0, d1, __uint_as_float(pv[c + e]), __uint_as_float(pv[c + e + 1]), x0, x1);
-            pp[e / 2] = pack_bf16x2(x0, x1);
-            dd[e / 2] = pack_bf16x2(d0, d1);
+            const uint32_t keep = pair_mask(b, e);
+            pp[e / 2] &= keep;
+            dd[e / 2] &= keep;
           }
-          if (!full) {
-            // Rows that do not see the key: zero halves of the packed pairs.
-            const uint32_t b = ~first_bits(key - i0 - c) &
-                               (first_bits(key + p.window - i0 - c) | (key < p.sink ? 0xFFFFFFFFu : 0u));
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint32_t keep = pair_mask(b, e);
-              pp[e / 2] &= keep;
-              dd[e / 2] &= keep;
-            }
-          }
-          tmem_st16(tS + c / 2, pp);
-          tmem_st16(tS + 32 + c / 2, dd);
         }
+        // Over the 32 columns of scores that this group has read itself: P^T, dS^T.
+        tmem_st16(tS + sub, pp);
+        tmem_st16(tS + sub + 16, dd);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ds_full[grp][sc & 1]);
+        if (lane == 0) mbar_arrive(&bar.ds_full[x][sc & 1]);
       }
       if (!ok) break;
       if (!(ok = mbar_wait_warp(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9))) break;
       ++an;
       tc_fence_after();
-      // Group 0 writes dK, group 1 dV.
-      const bool isk = grp == 0;
+      // Groups 0 and 1 write dK, groups 2 and 3 dV, every other 16 columns each.
+      const bool isk = x == 0;
       const uint32_t ta = isk ? tK : tV;
       const float scl = isk ? p.scale : 1.f;
       if (w.part < 0) {
@@ -737,16 +730,18 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                             : p.dv + (int64_t)w.b * p.dv_sb + (int64_t)w.hk * p.dv_sh + (int64_t)key * p.dv_sn;
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
+          if ((c / 16 & 1) != (grp & 1)) continue;
           uint32_t o[16];
           tmem_ld16(ta + c, o);
           tmem_wait_ld();
           if (key < p.N) store16(dst + c, o, scl);
         }
       } else {
-        float *dst = p.part + (((((int64_t)w.b * p.hkv + w.hk) * p.nst + w.kt) * (1 + p.nseg) + w.part) * 2 + grp) *
+        float *dst = p.part + (((((int64_t)w.b * p.hkv + w.hk) * p.nst + w.kt) * (1 + p.nseg) + w.part) * 2 + x) *
                                   (kTileKeys * D) + r * D;
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
+          if ((c / 16 & 1) != (grp & 1)) continue;
           uint32_t o[16];
           tmem_ld16(ta + c, o);
           tmem_wait_ld();
@@ -811,14 +806,14 @@ static cudaError_t launch_swa_bwd_d(const CUtensorMap *m, const SwaBwdParams &p,
   e = cudaFuncSetAttribute(swa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaDqCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.batch * p.hq * p.nt;
-  swa_bwd_dq_kernel<D><<<(int)(items < nsm ? items : nsm), kSwaThreads, SwaDqCfg<D>::SMEM, st>>>(
+  swa_bwd_dq_kernel<D><<<(int)(items < nsm ? items : nsm), kSwaBwdThreads, SwaDqCfg<D>::SMEM, st>>>(
       m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
   e = cudaFuncSetAttribute(swa_bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaDkvCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.batch * p.hkv * (p.nst * p.nseg + p.nt);
-  swa_bwd_dkdv_kernel<D><<<(int)(units < nsm ? units : nsm), kSwaThreads, SwaDkvCfg<D>::SMEM, st>>>(
+  swa_bwd_dkdv_kernel<D><<<(int)(units < nsm ? units : nsm), kSwaBwdThreads, SwaDkvCfg<D>::SMEM, st>>>(
       m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
 

@@ -28,16 +28,17 @@ struct SwaTile {
 constexpr uint32_t kHi128 = desc_hi(1024, kSwizzle128), kHi32 = desc_hi(256, kSwizzle32);
 
 // D[tmem, D columns] (+)= A[tmem] B over the tile's rows [64 half, 64 half + 64): four steps
-// of 16 rows, A's in consecutive groups of 8 columns.  fresh: the first step overwrites.
-template <int D>
+// of 16 rows, A's in groups of 8 columns, two by two, GAP columns between the pairs.  fresh:
+// the first step overwrites.
+template <int D, int GAP = 0>
 __device__ __forceinline__ void swa_acc(uint32_t d, uint32_t a, uint32_t tile, int half, bool fresh) {
   const uint32_t b = desc_lo(tile, D == 128 ? SwaTile<D>::R0 : 16) + half * 512;
   const uint32_t b1 = desc_lo(tile + SwaTile<D>::R0, 16) + half * 128;
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
     const uint32_t acc = (kk == 0 && fresh) ? 0u : 1u;
-    umma_ts_w(d, a + kk * 8, b + kk * 128, kHi128, idesc_bf16(128, D == 128 ? 128 : 64, 0, 1), acc);
-    if (D == 80) umma_ts_w(d + 64, a + kk * 8, b1 + kk * 32, kHi32, idesc_bf16(128, 16, 0, 1), acc);
+    umma_ts_w(d, a + kk * 8 + (kk >> 1) * GAP, b + kk * 128, kHi128, idesc_bf16(128, D == 128 ? 128 : 64, 0, 1), acc);
+    if (D == 80) umma_ts_w(d + 64, a + kk * 8 + (kk >> 1) * GAP, b1 + kk * 32, kHi32, idesc_bf16(128, 16, 0, 1), acc);
   }
 }
 
