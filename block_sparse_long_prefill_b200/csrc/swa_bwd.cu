@@ -170,21 +170,23 @@ struct SwaBars {
   // write-back is waited for, so two write-backs may complete before that wait looks.
   uint64_t s_full[2], p_empty[2], ds_full[2][2];
   uint64_t slot_empty[3];              // a write-back's slot consumed
+  uint64_t kv_ready;                   // a unit's K and V in TMEM
   uint64_t acc_full[2], acc_empty[2];  // accumulators final / read out
   uint64_t mma_done[2];                // per issuing warp
   uint32_t tmem_base;
   int abort;
 };
 
-// warps: elementwise warps that arrive on the barriers of a step (each once).
-__device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps) {
+// warps: elementwise warps that arrive on the barriers of a step (each once); k_readers:
+// arrivals that free a K stage.
+__device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps, int k_readers) {
   for (int s = 0; s < 4; ++s) {
     mbar_init(&bar.q_full[s], 1);
     mbar_init(&bar.q_empty[s], 1);
   }
   for (int s = 0; s < 5; ++s) {
     mbar_init(&bar.k_full[s], 1);
-    mbar_init(&bar.k_empty[s], 1);
+    mbar_init(&bar.k_empty[s], k_readers);
     mbar_init(&bar.v_full[s], 1);
     mbar_init(&bar.v_empty[s], 1);
   }
@@ -197,6 +199,7 @@ __device__ __forceinline__ void swa_init_bars(SwaBars &bar, int warps) {
     mbar_init(&bar.acc_empty[x], 16);
   }
   for (int x = 0; x < 3; ++x) mbar_init(&bar.slot_empty[x], 1);
+  mbar_init(&bar.kv_ready, 16);
   mbar_init(&bar.mma_done[0], 1);
   mbar_init(&bar.mma_done[1], 1);
   bar.abort = 0;
@@ -222,7 +225,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   constexpr uint32_t FULL = 0xffffffffu;
   const int nitems = p.batch * p.hq * p.nt;
 
-  if (tid == 0) swa_init_bars(bar, 16);
+  if (tid == 0) swa_init_bars(bar, 16, 1);
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmG);
@@ -380,7 +383,8 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_empty[0]);
-        // The dS slot's last product is done (it was issued a step ago).
+        // The dS slot's last product is done (it was issued a step ago; the S issuer waiting
+        // for it instead delays the next products: 2135 cycles a tile, not 1892).
         if (!(ok = mbar_wait_warp(&bar.slot_empty[sc & 1], ((sc >> 1) & 1) ^ 1, abort, p.status, site0 + 11))) break;
         uint32_t ds[16];
 #pragma unroll
@@ -469,16 +473,21 @@ __device__ __forceinline__ bool swa_dkv_unit(const SwaBwdParams &p, int u, SwaDk
   return w.t0 < w.t1;
 }
 
-// TMEM of the dK / dV kernel: the halves' S in a ring of `S` slots of 64 columns (P and dS
-// are written back over them), their dP in a ring of two, then the accumulators.  With
-// three S slots a half's products are issued as soon as its group has read its last half
-// into registers, while it still computes; dK and dV of 128 columns leave room for two, and
-// a half's products wait for its group's write-back.
-template <int SLOTS>
+// TMEM of the dK / dV kernel.  D = 64, 80: the halves' S in a ring of three slots of 64
+// columns (P and dS are written back over them), their dP in one slot (a half is read into
+// registers before the next one's products), the accumulators, and K, V and the blocks of
+// ones as the products' left operands: from shared memory a 64-column product takes 48
+// cycles instead of 32, and the loads of the query tiles compete for the same bandwidth
+// (measured at D = 80: 2708 cycles a tile).  D = 128: accumulators of 256 columns leave room
+// for two S and two dP slots only; K and V stay in shared memory.
+template <int D>
 struct SwaTmem {
-  static constexpr int S = SLOTS;
-  static constexpr uint32_t P0 = 64 * S, ACC = P0 + 128;
+  static constexpr bool KV = D != 128;
+  static constexpr int S = KV ? 3 : 2, P = KV ? 1 : 2;
+  static constexpr uint32_t P0 = 64 * S, ACC = 64 * (S + P), K = ACC + 2 * D, V = K + D / 2, ONE = V + D / 2;
+  static_assert((KV ? ONE + 16 : K) <= 512, "TMEM columns");
   static __device__ __forceinline__ uint32_t s_at(uint32_t h) { return 64 * (h % S); }
+  static __device__ __forceinline__ uint32_t p_at(uint32_t h) { return P0 + 64 * (h % P); }
 };
 
 template <int D>
@@ -494,8 +503,7 @@ struct SwaDkvCfg {
   static constexpr int BAR_OFF = ONE_OFF + 2 * kSwaExtra;
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
-  using M = SwaTmem<D == 128 ? 2 : 3>;
-  static_assert(M::ACC + 2 * D <= 512, "TMEM columns");
+  using M = SwaTmem<D>;
 };
 
 template <int D>
@@ -517,9 +525,10 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   constexpr uint32_t FULL = 0xffffffffu;
   const int nunits = swa_dkv_units(p);
 
-  if (tid == 0) swa_init_bars(bar, 8);
+  using M = typename C::M;
+  if (tid == 0) swa_init_bars(bar, 8, M::KV ? 16 : 1);   // (K, V staged: every elementwise warp)
   // The blocks of ones: columns 0 - 2 (lse) and 3 - 5 (D).
-  for (int r = tid; r < 2 * 128; r += kSwaBwdThreads) {
+  for (int r = tid; !M::KV && r < 2 * 128; r += kSwaBwdThreads) {
     unsigned char *blk = sbase + C::ONE_OFF + (r >> 7) * kSwaExtra;
     const uint4 ones = r < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u);
     *reinterpret_cast<uint4 *>(blk + extra_offset(r & 127, 0)) = ones;
@@ -588,16 +597,17 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S^T and dP^T
-    // Per query tile and half x, as soon as its group has read its last half's into
-    // registers and the S slot's write-back has been consumed.
-    using M = typename C::M;
+    // Per query tile and half x: S^T as soon as the S slot's write-back has been consumed,
+    // dP^T as soon as its slot has been read into registers.
     uint32_t step = 0, kn = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
       SwaDkvUnit w;
       if (!swa_dkv_unit(p, u, w)) continue;
       const uint32_t ks = kn % C::KS;
-      if (!(ok = mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3))) break;
+      if (M::KV) ok = mbar_wait_warp(&bar.kv_ready, kn & 1, abort, p.status, site0 + 3);
+      else ok = mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3);
+      if (!ok) break;
       ++kn;
       const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
       for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
@@ -607,14 +617,23 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         for (int x = 0; x < 2; ++x) {
           const uint32_t h = 2 * step + x;
           if (!(ok = mbar_wait_warp(&bar.slot_empty[h % M::S], ((h / M::S) & 1) ^ 1, abort, p.status, site0 + 11))) break;
-          if (!(ok = mbar_wait_warp(&bar.p_empty[x], (step & 1) ^ 1, abort, p.status, site0 + 10))) break;
+          const uint32_t qt = base + C::Q_OFF + st * T::TILE, gt = base + C::DO_OFF + st * T::TILE;
           tc_fence_after();
           if (elect_one()) {
-            swa_scores<D, 64>(tmem + M::s_at(h), kt, base + C::Q_OFF + st * T::TILE, 64 * x, base + C::ONE_OFF, ex);
-            swa_scores<D, 64>(tmem + M::P0 + 64 * x, vt, base + C::DO_OFF + st * T::TILE, 64 * x,
-                              base + C::ONE_OFF + kSwaExtra, ex);
+            if constexpr (M::KV) swa_scores_tmem<D, 64>(tmem + M::s_at(h), tmem + M::K, qt, 64 * x, tmem + M::ONE, ex);
+            else swa_scores<D, 64>(tmem + M::s_at(h), kt, qt, 64 * x, base + C::ONE_OFF, ex);
+          }
+          __syncwarp();
+          // (One dP slot: read by the half before; two: by the group's own last half.)
+          if (!(ok = M::P == 1 ? mbar_wait_warp(&bar.p_empty[0], (h & 1) ^ 1, abort, p.status, site0 + 10)
+                               : mbar_wait_warp(&bar.p_empty[x], (step & 1) ^ 1, abort, p.status, site0 + 10)))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+            if constexpr (M::KV) swa_scores_tmem<D, 64>(tmem + M::p_at(h), tmem + M::V, gt, 64 * x, tmem + M::ONE + 8, ex);
+            else swa_scores<D, 64>(tmem + M::p_at(h), vt, gt, 64 * x, base + C::ONE_OFF + kSwaExtra, ex);
             umma_commit(&bar.s_full[x]);
-            if (x == 1 && t == w.t1 - 1) umma_commit(&bar.k_empty[ks]);
+            if (!M::KV && x == 1 && t == w.t1 - 1) umma_commit(&bar.k_empty[ks]);
           }
           __syncwarp();
         }
@@ -623,7 +642,6 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     swa_issued(&bar.mma_done[0], p.status);
   } else if (warp == 2) {
     // ------------------------------------------------------------ dV += P^T dO, dK += dS^T Q
-    using M = typename C::M;
     const uint32_t tK = tmem + M::ACC, tV = tK + D;
     uint32_t step = 0, an = 0;
     bool ok = true;
@@ -662,16 +680,63 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int q4 = warp & 3, grp = (warp - 4) >> 2;
     const int r = 32 * q4 + lane;                   // key of the tile == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    using M = typename C::M;
     const int x = grp >> 1, sub = 32 * (grp & 1);   // half of the tile, its first column there
-    const uint32_t tP = tmem + lane_off + M::P0 + 64 * x + sub;
     const uint32_t tK = tmem + lane_off + M::ACC, tV = tK + D;
     const float sl2 = p.scale_log2;
     uint32_t sc = 0, an = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < nunits; u += gridDim.x) {
-      SwaDkvUnit w;
-      if (!swa_dkv_unit(p, u, w)) continue;
+    SwaDkvUnit nw;
+    auto seek = [&](int v) {
+      while (v < nunits && !swa_dkv_unit(p, v, nw)) v += gridDim.x;
+      return v;
+    };
+    uint32_t kn = 0;
+    // A unit's K (groups 0, 1) and V (2, 3) from shared memory into TMEM, every other 16
+    // values of a row to a group, once the last unit's products have read what was there.
+    auto stage_kv = [&]() {
+      const uint32_t ks = kn % C::KS;
+      if (sc > 0 && !mbar_wait_warp(&bar.s_full[1], (sc - 1) & 1, abort, p.status, site0 + 12)) return false;
+      if (!mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 13)) return false;
+      tc_fence_after();
+      const unsigned char *tile = sbase + (x == 0 ? C::K_OFF : C::V_OFF) + ks * T::TILE;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        if ((j & 1) != (grp & 1)) continue;
+        uint32_t v[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = 2 * j + e;
+          const uint4 a = *reinterpret_cast<const uint4 *>(
+              c < 8 ? tile + r * 128 + ((c ^ (r & 7)) << 4) : tile + T::R0 + r * 32 + (((c - 8) ^ ((r >> 2) & 1)) << 4));
+          v[4 * e] = a.x;
+          v[4 * e + 1] = a.y;
+          v[4 * e + 2] = a.z;
+          v[4 * e + 3] = a.w;
+        }
+        tmem_st8(tmem + lane_off + (x == 0 ? M::K : M::V) + 8 * j, v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.k_empty[ks]);
+        mbar_arrive(&bar.kv_ready);
+      }
+      ++kn;
+      return true;
+    };
+    int u = seek(blockIdx.x);
+    if constexpr (M::KV) {
+      if (grp == 0) {
+        const uint32_t lse1[8] = {0x3F803F80u, 0x00003F80u, 0u, 0u, 0u, 0u, 0u, 0u};
+        const uint32_t d1[8] = {0u, 0x3F800000u, 0x3F803F80u, 0u, 0u, 0u, 0u, 0u};
+        tmem_st8(tmem + lane_off + M::ONE, lse1);
+        tmem_st8(tmem + lane_off + M::ONE + 8, d1);
+      }
+      if (u < nunits) ok = stage_kv();
+    }
+    while (ok && u < nunits) {
+      const SwaDkvUnit w = nw;
       const int key0 = w.kt * kTileKeys, key = key0 + r;
       int qt = w.first + w.t0 % w.len;
       for (int t = w.t0; t < w.t1; ++t, ++sc) {
@@ -683,11 +748,11 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const uint32_t tS = tmem + lane_off + M::s_at(2 * sc + x);
         uint32_t sv[32], pv[32];
         tmem_ld32(tS + sub, sv);
-        tmem_ld32(tP, pv);
+        tmem_ld32(tmem + lane_off + M::p_at(2 * sc + x) + sub, pv);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_empty[x]);
+        if (lane == 0) mbar_arrive(&bar.p_empty[M::P == 1 ? 0 : x]);
         uint32_t pp[16], dd[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -718,6 +783,10 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         if (lane == 0) mbar_arrive(&bar.ds_full[x][sc & 1]);
       }
       if (!ok) break;
+      u = seek(u + gridDim.x);
+      if constexpr (M::KV) {
+        if (u < nunits && !(ok = stage_kv())) break;
+      }
       if (!(ok = mbar_wait_warp(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9))) break;
       ++an;
       tc_fence_after();

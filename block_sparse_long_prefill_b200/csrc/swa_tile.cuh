@@ -61,6 +61,24 @@ __device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, i
   if (extra_a) umma_ss_w(d, desc_lo(extra_a, 16), kHi32, desc_lo(extra_b, 16) + row0 * 2, kHi32, id, 1u);
 }
 
+// The same with A in TMEM (D / 2 columns from a; its 16 more columns from extra_a): the
+// product then takes half of what shared memory has to feed it.
+template <int D, int NB>
+__device__ __forceinline__ void swa_scores_tmem(uint32_t d, uint32_t a, uint32_t b, int row0, uint32_t extra_a,
+                                                uint32_t extra_b) {
+  constexpr uint32_t id = idesc_bf16(128, NB, 0, 0);
+  const uint32_t bl = desc_lo(b, 16) + row0 * 8;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint32_t acc = ks > 0 ? 1u : 0u;
+    if (D == 80 && ks == 4)
+      umma_ts_w(d, a + ks * 8, desc_lo(b + SwaTile<D>::R0, 16) + row0 * 2, kHi32, id, acc);
+    else
+      umma_ts_w(d, a + ks * 8, bl + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128, id, acc);
+  }
+  umma_ts_w(d, extra_a, desc_lo(extra_b, 16) + row0 * 2, kHi32, id, 1u);
+}
+
 template <int D>
 __device__ __forceinline__ void swa_load_tile(unsigned char *dst, const CUtensorMap *m, const CUtensorMap *m1,
                                               uint64_t *bar, int row, int h, int b) {
