@@ -108,6 +108,22 @@ def _load():
 _lib = _load()
 
 
+def _load_binding():
+    """The compiled binding of the short calls (csrc/binding.cpp), beside the library."""
+    import importlib.util
+    path = os.path.join(_HERE, "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with "
+                          "`python -m block_sparse_long_prefill_b200.build` (nvcc, g++)")
+    spec = importlib.util.spec_from_file_location("_binding", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+_binding = _load_binding()
+
+
 def library() -> ctypes.CDLL:
     return _lib
 
@@ -167,33 +183,13 @@ def _stream(stream) -> ctypes.c_void_p:
     return stream.cuda_stream
 
 
-_HERE_ALREADY = contextlib.nullcontext()
+_NO_STREAM = contextlib.nullcontext()
 
 
-@contextlib.contextmanager
-def _moved(dev, stream):
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
-
-
-def _on(dev, stream):
-    """Makes ``dev`` the current device and ``stream`` (None: the device's current one) its
-    current stream, so that what a wrapper allocates belongs to the stream that uses it."""
-    if stream is None and torch.cuda.current_device() == dev.index:
-        return _HERE_ALREADY
-    return _moved(dev, stream)
-
-
-def _empty(shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _ptr(x):
-    return None if x is None else x.data_ptr()
+def _on_stream(stream):
+    """Makes ``stream`` (None: as it is) the current stream of its device, so that what a
+    call allocates belongs to the stream that uses it."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
 def workspace_size(batch, hq, hkv, N, d, block, topk) -> int:
@@ -302,25 +298,9 @@ def swa_attn_fwd_chunk(q, k, v, window: int, scale: float = 0.0, out=None, lse=N
                        sink: int = 0):
     """Sliding-window attention of the last N positions (q) over k.shape[2] positions, the
     first ``sink`` of them staying visible behind the window."""
-    b, hq, N, d = q.shape
-    hkv, Nk = k.shape[1], k.shape[2]
-    dev = _device("swa_attn_fwd", ("q", q, _BF16, False, None), ("k", k, _BF16, False, None),
-                  ("v", v, _BF16, False, tuple(k.shape)),
-                  ("out", out, _BF16, False, tuple(q.shape)),
-                  ("lse", lse, _F32, True, (b, hq, N)))
-    with _on(dev, None):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(b, hq, N, dtype=torch.float32, device=dev)
-        if sink:
-            _check("swa_sink_attn_fwd",
-                   _lib.swa_sink_attn_fwd(_t(q), _t(k), _t(v), b, hq, hkv, N, Nk, d, window, sink,
-                                          float(scale), _t(out), lse.data_ptr(), _stream(stream)))
-        else:
-            _check("swa_attn_fwd",
-                   _lib.swa_attn_fwd_chunk(_t(q), _t(k), _t(v), b, hq, hkv, N, Nk, d, window,
-                                           float(scale), _t(out), lse.data_ptr(), _stream(stream)))
+    with _on_stream(stream):
+        rc, out, lse = _binding.swa_fwd(q, k, v, window, sink, scale, out, lse)
+    _check("swa_attn_fwd", rc)
     return out, lse
 
 
@@ -336,42 +316,10 @@ def swa_attn_bwd(q, k, v, out, lse, dout, window: int, sink: int = 0, scale: flo
                  dk=None, dv=None, workspace=None, stream=None):
     """Gradients of swa_attn_fwd (``window``, ``sink`` and ``scale`` as given to it) for whole
     sequences.  Returns (dq, dk, dv), bf16."""
-    b, hq, N, d = q.shape
-    hkv = k.shape[1]
-    kshape = (b, hkv, N, d)
-    dev = _device("swa_attn_bwd", ("q", q, _BF16, False, None), ("k", k, _BF16, False, kshape),
-                  ("v", v, _BF16, False, kshape), ("out", out, _BF16, False, tuple(q.shape)),
-                  ("lse", lse, _F32, True, (b, hq, N)), ("dout", dout, _BF16, False, tuple(q.shape)),
-                  ("dq", dq, _BF16, False, tuple(q.shape)), ("dk", dk, _BF16, False, kshape),
-                  ("dv", dv, _BF16, False, kshape), ("workspace", workspace, None, True, None))
-    with _on(dev, stream):
-        dq = _empty(q.shape, _BF16, dev) if dq is None else dq
-        dk = _empty(kshape, _BF16, dev) if dk is None else dk
-        dv = _empty(kshape, _BF16, dev) if dv is None else dv
-        if workspace is None:
-            workspace = _empty((swa_bwd_workspace_size(b, hq, hkv, N, d, window, sink),), torch.uint8, dev)
-        _check("swa_attn_bwd",
-               _lib.swa_attn_bwd(_t(q), _t(k), _t(v), _t(out), _t(dout), lse.data_ptr(), b, hq, hkv, N,
-                                 d, window, sink, float(scale), _t(dq), _t(dk), _t(dv),
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 _stream(None)))
+    with _on_stream(stream):
+        rc, dq, dk, dv = _binding.swa_bwd(q, k, v, out, lse, dout, window, sink, scale, dq, dk, dv, workspace)
+    _check("swa_attn_bwd", rc)
     return dq, dk, dv
-
-
-def _angles(fn, cos, sin):
-    """The device checks' specs of an angle table, and (rot, positions) of it."""
-    if cos.dim() != 2:
-        raise ValueError(f"{fn}: cos and sin are [positions, rot / 2]")
-    specs = (("cos", cos, _F32, True, None), ("sin", sin, _F32, True, tuple(cos.shape)))
-    return specs, 2 * cos.shape[1], cos.shape[0]
-
-
-def _weight(fn, name, w, d):
-    if w is None:
-        return (name, None, None, True, None), MobaWeight(None, 0)
-    if w.dtype not in (_BF16, _F32):
-        raise ValueError(f"{fn}: {name} must be torch.bfloat16 or torch.float32, not {w.dtype}")
-    return (name, w, w.dtype, True, (d,)), MobaWeight(w.data_ptr(), int(w.dtype == _F32))
 
 
 def qk_norm_rope_fwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -381,22 +329,10 @@ def qk_norm_rope_fwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=Non
     float32 [positions, rot / 2]; the first rot columns turn, in pairs (i, i + rot / 2) or,
     interleaved, of neighbours.  positions: int32 [b, N] (default: row n is at n).  Returns
     (q_out [b, hq, N, d], k_out [b, hkv, N, d]) bf16, which may be given as q and k."""
-    fn = "qk_norm_rope_fwd"
-    b, hq, N, d = q.shape
-    hkv = k.shape[1]
-    table, rot, max_pos = _angles(fn, cos, sin)
-    sq, wq = _weight(fn, "q_weight", q_weight, d)
-    sk, wk = _weight(fn, "k_weight", k_weight, d)
-    kshape = (b, hkv, N, d)
-    dev = _device(fn, ("q", q, _BF16, False, None), ("k", k, _BF16, False, kshape), *table,
-                  ("positions", positions, _I32, True, (b, N)), sq, sk,
-                  ("q_out", q_out, _BF16, False, tuple(q.shape)), ("k_out", k_out, _BF16, False, kshape))
-    with _on(dev, stream):
-        q_out = _empty(q.shape, _BF16, dev) if q_out is None else q_out
-        k_out = _empty(kshape, _BF16, dev) if k_out is None else k_out
-        _check(fn, _lib.qk_norm_rope_fwd(_t(q), _t(k), cos.data_ptr(), sin.data_ptr(), _ptr(positions),
-                                         wq, wk, b, hq, hkv, N, d, rot, max_pos, int(interleaved),
-                                         float(eps), _t(q_out), _t(k_out), _stream(None)))
+    with _on_stream(stream):
+        rc, q_out, k_out = _binding.rope_fwd(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved,
+                                             q_out, k_out)
+    _check("qk_norm_rope_fwd", rc)
     return q_out, k_out
 
 
@@ -406,47 +342,11 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=No
     """Gradients of qk_norm_rope_fwd for the gradients dq_out, dk_out of its results and its
     inputs q, k.  Returns (dq, dk, dq_weight, dk_weight): bf16, and float32 [d] or None where
     there is no weight."""
-    fn = "qk_norm_rope_bwd"
-    b, hq, N, d = dq_out.shape
-    hkv = dk_out.shape[1]
-    table, rot, max_pos = _angles(fn, cos, sin)
-    sq, wq = _weight(fn, "q_weight", q_weight, d)
-    sk, wk = _weight(fn, "k_weight", k_weight, d)
-    qshape, kshape = (b, hq, N, d), (b, hkv, N, d)
-    dev = _device(fn, ("dq_out", dq_out, _BF16, False, None), ("dk_out", dk_out, _BF16, False, kshape),
-                  ("q", q, _BF16, False, qshape), ("k", k, _BF16, False, kshape), *table,
-                  ("positions", positions, _I32, True, (b, N)), sq, sk,
-                  ("dq", dq, _BF16, False, qshape), ("dk", dk, _BF16, False, kshape),
-                  ("workspace", workspace, None, True, None))
-    with _on(dev, stream):
-        dq = _empty(qshape, _BF16, dev) if dq is None else dq
-        dk = _empty(kshape, _BF16, dev) if dk is None else dk
-        dqw = _empty((d,), _F32, dev) if q_weight is not None else None
-        dkw = _empty((d,), _F32, dev) if k_weight is not None else None
-        if workspace is None and (dqw is not None or dkw is not None):
-            size = ctypes.c_size_t(0)
-            _check("qk_norm_rope_bwd_workspace_size",
-                   _lib.qk_norm_rope_bwd_workspace_size(b, hq, hkv, N, d, ctypes.byref(size)))
-            workspace = _empty((size.value,), torch.uint8, dev)
-        _check(fn, _lib.qk_norm_rope_bwd(_t(dq_out), _t(dk_out), _t(q), _t(k), cos.data_ptr(),
-                                         sin.data_ptr(), _ptr(positions), wq, wk, b, hq, hkv, N, d, rot,
-                                         max_pos, int(interleaved), float(eps), _t(dq), _t(dk), _ptr(dqw),
-                                         _ptr(dkw), _ptr(workspace),
-                                         0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                         _stream(None)))
-    return dq, dk, dqw, dkw
-
-
-def _tokens(x):
-    """[tokens, heads, d] -> moba_tensor with sn between tokens and sh between heads."""
-    if x is None:
-        return MobaTensor(None, 0, 0, 0)
-    st = x.stride()
-    if len(st) != 3:
-        raise ValueError("expected a [tokens, heads, d] tensor")
-    if st[2] != 1:
-        raise ValueError("the head dimension must be contiguous")
-    return MobaTensor(x.data_ptr(), 0, st[1], st[0])
+    with _on_stream(stream):
+        rc, dq, dk, dq_weight, dk_weight = _binding.rope_bwd(dq_out, dk_out, q, k, cos, sin, positions, q_weight,
+                                                             k_weight, eps, interleaved, dq, dk, workspace)
+    _check("qk_norm_rope_bwd", rc)
+    return dq, dk, dq_weight, dk_weight
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos=None, sin=None,
@@ -460,30 +360,10 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos
     b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (default: one token a sequence).
     With q [T, hq, d], returns the queries normalised and rotated to the same positions
     (tokens behind the last sequence are left as they were), else None."""
-    fn = "kv_append"
-    T, hkv, d = k.shape
-    pages, _, page, _ = k_pages.shape
-    batch, max_pages = page_table.shape
-    table, rot, max_pos = ((), 0, 0) if cos is None and sin is None else _angles(fn, cos, sin)
-    sq, wq = _weight(fn, "q_weight", q_weight, d)
-    sk, wk = _weight(fn, "k_weight", k_weight, d)
-    pshape = (pages, hkv, page, d)
-    dev = _device(fn, ("k", k, _BF16, False, None), ("v", v, _BF16, False, tuple(k.shape)),
-                  ("k_pages", k_pages, _BF16, False, pshape), ("v_pages", v_pages, _BF16, False, pshape),
-                  ("page_table", page_table, _I32, True, None), ("seq_lens", seq_lens, _I32, True, (batch,)),
-                  ("cu_seqlens", cu_seqlens, _I32, True, (batch + 1,)), *table, sq, sk,
-                  ("q", q, _BF16, False, None if q is None else (T, q.shape[1], d)),
-                  ("q_out", q_out, _BF16, False, None if q is None else tuple(q.shape)))
-    if q is None and (q_out is not None or q_weight is not None):
-        raise ValueError(f"{fn}: q_out and q_weight need q")
-    with _on(dev, stream):
-        if q is not None and q_out is None:
-            q_out = _empty(q.shape, _BF16, dev)
-        _check(fn, _lib.kv_append(_tokens(k), _tokens(v), _tokens(q), _ptr(cu_seqlens), seq_lens.data_ptr(),
-                                  page_table.data_ptr(), _ptr(cos), _ptr(sin), wq, wk, batch, T,
-                                  0 if q is None else q.shape[1], hkv, d, rot, max_pos, int(interleaved),
-                                  float(eps), page, pages, max_pages, _t(k_pages), _t(v_pages),
-                                  _tokens(q_out), _stream(None)))
+    with _on_stream(stream):
+        rc, q_out = _binding.append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, cos, sin, k_weight,
+                                    eps, interleaved, q, q_weight, q_out)
+    _check("kv_append", rc)
     return q_out
 
 
@@ -495,43 +375,16 @@ def paged_decode_workspace_size(batch, hq, hkv, d) -> int:
     return out.value
 
 
-def _rows(x):
-    """[sequences, heads, d] -> moba_tensor with sb between sequences and sh between heads."""
-    st = x.stride()
-    if len(st) != 3:
-        raise ValueError("expected a [batch, heads, d] tensor")
-    if st[2] != 1:
-        raise ValueError("the head dimension must be contiguous")
-    return MobaTensor(x.data_ptr(), st[0], st[1], 0)
-
-
 def paged_decode_attn(q, k_pages, v_pages, page_table, seq_lens, window: int = 0, sink: int = 0,
                       scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
     """Attention of one new token per sequence, q [batch, hq, d], over the paged cache of
     kv_append ([MoBA] §실험: block-sparse prefill, full attention while decoding; with a
     window, what swa_attn_fwd computes for the last position).  The query of sequence b sits
     at position seq_lens[b] - 1.  Returns (out bf16 [batch, hq, d], lse float32 [batch, hq])."""
-    fn = "paged_decode_attn"
-    batch, hq, d = q.shape
-    pages, hkv, page, _ = k_pages.shape
-    pshape = (pages, hkv, page, d)
-    dev = _device(fn, ("q", q, _BF16, False, None), ("k_pages", k_pages, _BF16, False, pshape),
-                  ("v_pages", v_pages, _BF16, False, pshape), ("page_table", page_table, _I32, True, None),
-                  ("seq_lens", seq_lens, _I32, True, (batch,)), ("out", out, _BF16, False, tuple(q.shape)),
-                  ("lse", lse, _F32, True, (batch, hq)), ("workspace", workspace, None, True, None))
-    if page_table.dim() != 2 or page_table.shape[0] != batch:
-        raise ValueError(f"{fn}: page_table is [batch, pages of a sequence]")
-    with _on(dev, stream):
-        out = _empty(q.shape, _BF16, dev) if out is None else out
-        lse = _empty((batch, hq), _F32, dev) if lse is None else lse
-        if workspace is None:
-            workspace = _empty((paged_decode_workspace_size(batch, hq, hkv, d),), torch.uint8, dev)
-
-        _check(fn, _lib.paged_decode_attn(_rows(q), _t(k_pages), _t(v_pages), page_table.data_ptr(),
-                                          seq_lens.data_ptr(), batch, hq, hkv, d, page, pages,
-                                          page_table.shape[1], window, sink, float(scale), _rows(out),
-                                          lse.data_ptr(), workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(), _stream(None)))
+    with _on_stream(stream):
+        rc, out, lse = _binding.decode(q, k_pages, v_pages, page_table, seq_lens, window, sink, scale, out, lse,
+                                       workspace)
+    _check("paged_decode_attn", rc)
     return out, lse
 
 

@@ -1,4 +1,5 @@
-"""Build libmoba.so (the sm_100a CUDA kernels and their C ABI) in-tree with nvcc."""
+"""Build libmoba.so (the sm_100a CUDA kernels and their C ABI) with nvcc and the compiled
+binding of its short calls with the host compiler, both in-tree."""
 import os
 import shutil
 import subprocess
@@ -9,6 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoba.so")
+BINDING = os.path.join(PKG, "_binding.so")   # the compiled binding of the short calls (binding.cpp)
 SOURCES = ["api.cu", "select.cu", "gate.cu", "attn.cu", "merge.cu", "noalloc.cu", "bwd.cu",
            "swa_fwd.cu", "swa_bwd.cu", "rope.cu", "decode.cu"]
 HEADERS = ["common.cuh", "params.h", "lists.cuh", "rows.cuh", "swa_tile.cuh"]
@@ -28,19 +30,46 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _older(target: str, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target) for p in deps)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "moba.h")]
-    return any(os.path.getmtime(p) > t for p in deps)
+    return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "moba.h")])
+
+
+def _build_binding(verbose: bool = False) -> None:
+    """Compile _binding.so against the installed torch; it finds libmoba.so beside itself."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", cuda,
+           *[f for p in include_paths() for f in ("-isystem", p)],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", PKG, "-l:libmoba.so", "-Wl,-rpath,$ORIGIN",
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile libmoba.so for sm_100a (cross-compiles without a GPU).  Each source is
-    compiled to an object file in parallel, then the objects are linked."""
-    if not force and not _stale():
-        return LIB
+    """Compile libmoba.so for sm_100a (cross-compiles without a GPU) and its binding.  Each
+    source is compiled to an object file in parallel, then the objects are linked."""
+    if force or _stale():
+        _build_library(verbose, extra)
+    if force or _older(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "moba.h")]):
+        _build_binding(verbose)
+    return LIB
+
+
+def _build_library(verbose: bool, extra) -> None:
     from concurrent.futures import ThreadPoolExecutor
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -66,7 +95,6 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     for o in objs:
         os.remove(o)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
