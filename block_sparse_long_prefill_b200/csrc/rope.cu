@@ -191,9 +191,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_fwd_kernel(const
   const bool in = v < LPR;
   const int cq = (p.hq + hpt - 1) / hpt, ck = (p.hkv + hpt - 1) / hpt;
   const int groups = (p.N + RPW - 1) / RPW;
-  const long long task = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int hc = (int)(task % (cq + ck));
-  const long long tg = task / (cq + ck);
+  // The block's warps take neighbouring tokens of the same heads, so that head-major rows are
+  // written in runs of kRopeWarps warps.
+  const int hc = (int)(blockIdx.x % (unsigned)(cq + ck));
+  const long long tg = (long long)(blockIdx.x / (unsigned)(cq + ck)) * kRopeWarps + (threadIdx.x >> 5);
   const int b = (int)(tg / groups);
   if (b >= p.batch) return;
   const int n = (int)(tg % groups) * RPW + sub;
@@ -413,9 +414,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kv_append_kernel(const Append
   const int vv = in ? v : 0;
   const int cq = p.q.ptr ? (p.hq + hpt - 1) / hpt : 0;
   const int ck = (p.hkv + hpt - 1) / hpt;
-  const long long task = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int hc = (int)(task % (cq + 2 * ck));
-  const long long t0 = task / (cq + 2 * ck) * RPW;
+  const int hc = (int)(blockIdx.x % (unsigned)(cq + 2 * ck));
+  const long long t0 = ((long long)(blockIdx.x / (unsigned)(cq + 2 * ck)) * kRopeWarps + (threadIdx.x >> 5)) * RPW;
   if (t0 >= p.T) return;
   const int t = (int)t0 + sub;
   const int which = hc < cq ? 0 : (hc < cq + ck ? 1 : 2);   // q, k, v
@@ -500,7 +500,7 @@ static cudaError_t launch_rope_fwd_d(const RopeParams &p, cudaStream_t st) {
   const long long groups = (long long)((p.N + RowLanes<D>::RPW - 1) / RowLanes<D>::RPW) * p.batch;
   const int hpt = rope_heads(groups, p.hq + p.hkv);
   const long long chunks = (p.hq + hpt - 1) / hpt + (p.hkv + hpt - 1) / hpt;
-  qk_norm_rope_fwd_kernel<D><<<rope_blocks(chunks * groups), kRopeThreads, 0, st>>>(p, hpt);
+  qk_norm_rope_fwd_kernel<D><<<(unsigned)(chunks * rope_blocks(groups)), kRopeThreads, 0, st>>>(p, hpt);
   return cudaGetLastError();
 }
 
@@ -548,7 +548,7 @@ static cudaError_t launch_append_d(const AppendParams &p, cudaStream_t st) {
   const int hpt = rope_heads(groups, (p.q.ptr ? p.hq : 0) + 2 * p.hkv);
   const long long ck = (p.hkv + hpt - 1) / hpt;
   const long long cq = p.q.ptr ? (p.hq + hpt - 1) / hpt : 0;
-  kv_append_kernel<D><<<rope_blocks((cq + 2 * ck) * groups), kRopeThreads, 0, st>>>(p, hpt);
+  kv_append_kernel<D><<<(unsigned)((cq + 2 * ck) * rope_blocks(groups)), kRopeThreads, 0, st>>>(p, hpt);
   return cudaGetLastError();
 }
 
