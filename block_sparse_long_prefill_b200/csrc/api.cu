@@ -227,8 +227,8 @@ int check_rope(const float *cosp, const float *sinp, const int32_t *positions, c
                const moba_weight &kw, int batch, int hq, int hkv, int N, int d, int rot, int max_pos,
                int interleaved, float eps) {
   if (batch < 1 || hq < 1 || hkv < 1 || N < 1 || max_pos < 1) return MOBA_ERR_SHAPE;
-  // Row groups of all heads are counted as blocks of one grid dimension.
-  if ((double)batch * N * ((double)hq + hkv) >= 8.0 * 2147483647.0) return MOBA_ERR_SHAPE;
+  // Groups of rows are counted in 32 bits, and as blocks of one grid dimension.
+  if ((double)batch * N * ((double)hq + hkv) >= 8589934592.0) return MOBA_ERR_SHAPE;
   int rc = check_attn_dim(d);
   if (rc) return rc;
   if (rot < 16 || rot > d || rot % 16) return MOBA_ERR_DIM;

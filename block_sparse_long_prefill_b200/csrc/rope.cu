@@ -45,6 +45,55 @@ __device__ __forceinline__ void load_weight(const RopeWeight &w, int c0, float (
   }
 }
 
+// A vector's eight values as pairs for the packed fp32 instructions (each half rounded as
+// the scalar instruction would).
+struct Vec8 {
+  float2 v[4];
+};
+__device__ __forceinline__ Vec8 unpack_v(const uint4 &a) {
+  Vec8 x;
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    x.v[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+  return x;
+}
+__device__ __forceinline__ uint4 pack_v(const Vec8 &x) {
+  return make_uint4(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y),
+                    pack_bf16x2(x.v[2].x, x.v[2].y), pack_bf16x2(x.v[3].x, x.v[3].y));
+}
+__device__ __forceinline__ Vec8 to_v(const float (&x)[8]) {
+  Vec8 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y.v[e] = make_float2(x[2 * e], x[2 * e + 1]);
+  return y;
+}
+__device__ __forceinline__ Vec8 mul_v(const Vec8 &a, const Vec8 &b) {
+  Vec8 c;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c.v[e] = __fmul2_rn(a.v[e], b.v[e]);
+  return c;
+}
+__device__ __forceinline__ Vec8 mul_v(const Vec8 &a, float b) {
+  Vec8 c;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c.v[e] = __fmul2_rn(a.v[e], make_float2(b, b));
+  return c;
+}
+__device__ __forceinline__ Vec8 fma_v(const Vec8 &a, const Vec8 &b, const Vec8 &c) {
+  Vec8 d;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d.v[e] = __ffma2_rn(a.v[e], b.v[e], c.v[e]);
+  return d;
+}
+__device__ __forceinline__ float dot_v(const Vec8 &a, const Vec8 &b) {
+  float2 s = __fmul2_rn(a.v[0], b.v[0]), t = __fmul2_rn(a.v[1], b.v[1]);
+  s = __ffma2_rn(a.v[2], b.v[2], s);
+  t = __ffma2_rn(a.v[3], b.v[3], t);
+  s = __fadd2_rn(s, t);
+  return s.x + s.y;
+}
+
 // A lane's place in the rotation: the lane that holds its columns' partners, and the
 // first pair of its angles.  Columns outside the rotation have themselves as partners.
 struct Place {
@@ -102,47 +151,37 @@ __device__ __forceinline__ void load_angles(const Place &pl, const float *cosp, 
   }
 }
 
-// The partner's values of a packed row vector (zero where a column has none, so that
-// infinities pass).
-__device__ __forceinline__ void mate8(const Place &pl, int interleaved, const uint4 &a,
-                                      const float (&x)[8], float (&y)[8]) {
+// The partner's values of a packed row vector x = unpack_v(a).  (Where a column has none
+// its factor is zero, and so is this, so that infinities pass.)
+__device__ __forceinline__ Vec8 mate_v(const Place &pl, int interleaved, const uint4 &a, const Vec8 &x) {
+  Vec8 y;
   if (interleaved) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+    for (int e = 0; e < 4; ++e) y.v[e] = make_float2(x.v[e].y, x.v[e].x);
   } else {
     uint4 b;
     b.x = __shfl_sync(kFull, a.x, pl.mate);
     b.y = __shfl_sync(kFull, a.y, pl.mate);
     b.z = __shfl_sync(kFull, a.z, pl.mate);
     b.w = __shfl_sync(kFull, a.w, pl.mate);
-    unpack8(b, y);
+    y = unpack_v(b);
   }
   if (pl.kind == 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+    for (int e = 0; e < 4; ++e) y.v[e] = make_float2(0.f, 0.f);
   }
+  return y;
 }
 
 // Normalise and rotate one row vector: y = (x cw + partner sw) rstd, cw and sw the lane's
 // angles times the weights of its own and of its partners' columns.
 template <int D>
 __device__ __forceinline__ uint4 turn_row(const uint4 &a, bool norm, const Place &pl, int interleaved,
-                                          int base, int v, float eps, const float (&cw)[8],
-                                          const float (&sw)[8]) {
-  float x[8], y[8], u[8];
-  unpack8(a, x);
-  mate8(pl, interleaved, a, x, y);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) u[e] = fmaf(y[e], sw[e], x[e] * cw[e]);
-  if (norm) {
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-    const float r = rsqrtf(row_sum<D>(ss, base, v) * (1.f / D) + eps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] *= r;
-  }
-  return pack8(u);
+                                          int base, int v, float eps, const Vec8 &cw, const Vec8 &sw) {
+  const Vec8 x = unpack_v(a);
+  Vec8 u = fma_v(mate_v(pl, interleaved, a, x), sw, mul_v(x, cw));
+  if (norm) u = mul_v(u, rsqrtf(row_sum<D>(dot_v(x, x), base, v) * (1.f / D) + eps));
+  return pack_v(u);
 }
 
 // The weights of a lane's columns and of its partners' columns.
@@ -159,17 +198,16 @@ __device__ __forceinline__ void load_weights(const RopeWeight &wt, const Place &
 
 // Angles times weights.
 __device__ __forceinline__ void load_factors(const Place &pl, const float *cosp, const float *sinp, int rot,
-                                             int pos, const RopeWeight &wt, int v, int lane, float (&cw)[8],
-                                             float (&sw)[8]) {
-  load_angles(pl, cosp, sinp, rot, pos, cw, sw);
+                                             int pos, const RopeWeight &wt, int v, int lane, Vec8 &cw, Vec8 &sw) {
+  float c[8], s[8];
+  load_angles(pl, cosp, sinp, rot, pos, c, s);
+  cw = to_v(c);
+  sw = to_v(s);
   if (wt.ptr) {
     float w[8], wm[8];
     load_weights(wt, pl, v, lane, w, wm);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cw[e] *= w[e];
-      sw[e] *= wm[e];
-    }
+    cw = mul_v(cw, to_v(w));
+    sw = mul_v(sw, to_v(wm));
   }
 }
 
@@ -218,7 +256,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_fwd_kernel(const
   uint4 *buf = slots[threadIdx.x >> 5];
   for (int h = 0; h < nh; ++h) cp_async_16(lane_slot(buf, h), row + h * src.sh);
   cp_async_commit();
-  float cw[8], sw[8];
+  Vec8 cw, sw;
   load_factors(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, wt, vv, lane, cw, sw);
   cp_async_wait_all();
 #pragma unroll 2
@@ -256,25 +294,30 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
     const RopeWeight wt = isq ? p.qw : p.kw;
     const bool norm = wt.ptr != nullptr;
     const int heads = isq ? p.hq : p.hkv, chunks = (heads + R - 1) / R;
-    float w[8], dw[8], c[8], s[8];
-    load_weight(wt, vv * 8, w);
+    Vec8 w, dw, c, s;                  // (s: the sines of R^T, their sign turned)
+    {
+      float x[8];
+      load_weight(wt, vv * 8, x);
+      w = to_v(x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[e] = 0.f;
+      for (int e = 0; e < 4; ++e) dw.v[e] = make_float2(0.f, 0.f);
+    }
     // Rounds in pairs: a warp takes the rounds 2 k, 2 k + 1 for k = gw, gw + nw, ...
-    const long long rounds = (long long)chunks * groups * p.batch;
-    auto after = [&](long long k) { return (k & 1) ? k + 2ll * nw - 1 : k + 1; };
+    // (Fewer than 2^30 by the call's check.)
+    const unsigned rounds = (unsigned)chunks * (unsigned)groups * (unsigned)p.batch;
+    auto after = [&](unsigned k) { return (k & 1) ? k + 2u * nw - 1u : k + 1u; };
     struct Round {
       int b, n, h0, nh, pos;
       bool live;
-      long long tg;
+      unsigned tg;
     };
-    auto decode = [&](long long k) {
+    auto decode = [&](unsigned k) {
       Round x;
-      x.tg = k / chunks;
+      x.tg = k / (unsigned)chunks;
       x.h0 = (int)(k - x.tg * chunks) * R;
       x.nh = min(R, heads - x.h0);
-      x.b = (int)(x.tg / groups);
-      x.n = (int)(x.tg - (long long)x.b * groups) * RPW + sub;
+      x.b = (int)(x.tg / (unsigned)groups);
+      x.n = (int)(x.tg - (unsigned)x.b * groups) * RPW + sub;
       x.live = in && x.n < p.N;
       x.pos = x.n;
       if (x.live && p.positions) x.pos = __ldg(p.positions + (int64_t)x.b * p.N + x.n);
@@ -293,7 +336,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
         if (norm) cp_async_16_zfill(lane_slot(to, R + i), r + i * src.sh, x.live);
       }
     };
-    long long k = 2ll * gw, tg = -1;
+    unsigned k = 2u * gw, tg = 0xFFFFFFFFu;
     Round cur{};
     if (k < rounds) {
       cur = decode(k);
@@ -301,45 +344,40 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
     }
     cp_async_commit();
     for (int buf = 0; k < rounds; buf ^= 1) {
-      const long long kn = after(k);
+      const unsigned kn = after(k);
       Round nx{};
       if (kn < rounds) {
         nx = decode(kn);
         issue(nx, buf ^ 1);
       }
       cp_async_commit();
-      if (cur.tg != tg) load_angles(pl, p.cosp, p.sinp, p.rot, cur.live ? cur.pos : 0, c, s);
-      tg = cur.tg;
+      if (cur.tg != tg) {
+        float x[8], y[8];
+        load_angles(pl, p.cosp, p.sinp, p.rot, cur.live ? cur.pos : 0, x, y);
+        c = to_v(x);
+        s = mul_v(to_v(y), -1.f);
+        tg = cur.tg;
+      }
       cp_async_wait_group<1>();
       uint16_t *out = dst.ptr + cur.b * dst.sb + (int64_t)cur.n * dst.sn + vv * 8 + cur.h0 * dst.sh;
       const uint4 *from = ring + buf * (2 * R * 32) + lane;
       for (int i = 0; i < cur.nh; ++i) {
         const uint4 ga = from[i * 32];
-        float dy[8], ym[8], g[8], x[8];
-        unpack8(ga, dy);
-        mate8(pl, p.interleaved, ga, dy, ym);
-        // R^T: the sines turn their sign.
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = fmaf(ym[e], -s[e], dy[e] * c[e]);
+        const Vec8 dy = unpack_v(ga);
+        Vec8 g = fma_v(mate_v(pl, p.interleaved, ga, dy), s, mul_v(dy, c));
         if (norm) {
-          unpack8(from[(R + i) * 32], x);
-          float ss = 0.f, gx = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = fmaf(x[e], x[e], ss);
-            gx = fmaf(g[e] * w[e], x[e], gx);
-          }
-          ss = row_sum<D>(ss, base, vv);
-          gx = row_sum<D>(gx, base, vv);
+          const Vec8 x = unpack_v(from[(R + i) * 32]), gw = mul_v(g, w);
+          const float ss = row_sum<D>(dot_v(x, x), base, vv);
+          const float gx = row_sum<D>(dot_v(gw, x), base, vv);
           const float r = rsqrtf(ss * (1.f / D) + p.eps);
-          const float m = gx * (1.f / D) * r * r;
+          const Vec8 xn = mul_v(x, r);
+          dw = fma_v(g, xn, dw);
+          const float m = -gx * (1.f / D) * r;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dw[e] = fmaf(g[e] * r, x[e], dw[e]);
-            g[e] = r * fmaf(-m, x[e], g[e] * w[e]);
-          }
+          for (int e = 0; e < 4; ++e)
+            g.v[e] = __fmul2_rn(__ffma2_rn(xn.v[e], make_float2(m, m), gw.v[e]), make_float2(r, r));
         }
-        if (cur.live) *reinterpret_cast<uint4 *>(out + i * dst.sh) = pack8(g);
+        if (cur.live) *reinterpret_cast<uint4 *>(out + i * dst.sh) = pack_v(g);
       }
       k = kn;
       cur = nx;
@@ -349,7 +387,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
     __syncthreads();
     if (in) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) part[warp * RPW + sub][vv * 8 + e] = dw[e];
+      for (int e = 0; e < 4; ++e) {
+        part[warp * RPW + sub][vv * 8 + 2 * e] = dw.v[e].x;
+        part[warp * RPW + sub][vv * 8 + 2 * e + 1] = dw.v[e].y;
+      }
     }
     __syncthreads();
     if (threadIdx.x < D) {
@@ -471,7 +512,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kv_append_kernel(const Append
     return;
   }
   const Place pl = place_of(vv, lane, p.cosp ? p.rot : 0, p.interleaved);
-  float cw[8], sw[8];
+  Vec8 cw, sw;
   load_factors(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, wt, vv, lane, cw, sw);
   cp_async_wait_all();
 #pragma unroll 2

@@ -44,13 +44,4 @@ __device__ __forceinline__ void unpack8(const uint4 &a, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint4 a;
-  a.x = pack_bf16x2(x[0], x[1]);
-  a.y = pack_bf16x2(x[2], x[3]);
-  a.z = pack_bf16x2(x[4], x[5]);
-  a.w = pack_bf16x2(x[6], x[7]);
-  return a;
-}
-
 }  // namespace moba
