@@ -11,8 +11,6 @@
 //                the own-block partial that the merge pass combines with the past-block
 //                partials (step 5).  SWA: the causal band of [SWA] §"슬라이딩 윈도우
 //                마스크", written straight to the output.
-//   kSinkBand    query-major SWA whose first `sink` keys stay visible: the chunks of the
-//                sinks that lie before the band, then the band's chunks.
 //   kGathered    gathered (row, q-head) pairs of one block-major list against the whole
 //                past block they picked (steps 3-4, causal=False); writes a normalised
 //                partial output and its log-sum-exp per (row, slot).
@@ -132,16 +130,14 @@ struct Tile {
 struct Unit {
   Tile t[2];
   int b, hk;
-  int key0;    // first key of chunk 0 (kSinkBand: of chunk ns)
+  int key0;    // first key of chunk 0
   int nc;      // chunks
-  int ns;      // kSinkBand: chunks of sinks before the band's (from key 0)
   int j;       // gathered: the past block
 };
 
 // Query-major units.  With GQA (G >= 2) a unit is two q-heads of one KV head at the
 // same rows; otherwise two consecutive row tiles of one head (MoBA: of one block),
 // attending to the union of their key ranges with per-row masks.
-template <int MODE>
 __device__ __forceinline__ void query_major_unit(const AttnParams &p, int u, Unit &w) {
   const int nq = (p.row_end - p.row_begin + kTileRows - 1) / kTileRows;
   int qt0, qt1, g0, g1, hb;
@@ -206,18 +202,6 @@ __device__ __forceinline__ void query_major_unit(const AttnParams &p, int u, Uni
   }
   w.key0 = lo;
   w.nc = (hi - lo) / kTileKeys + 1;
-  if constexpr (MODE == kSinkBand) {
-    // The sinks' chunks that lie before the band (the others are among the band's).
-    w.ns = min((p.sink + kTileKeys - 1) / kTileKeys, lo / kTileKeys);
-    w.nc += w.ns;
-  }
-}
-
-// First key of chunk m of a unit.
-template <int MODE>
-__device__ __forceinline__ int chunk_key(const Unit &w, int m) {
-  if constexpr (MODE == kSinkBand) return m < w.ns ? m * kTileKeys : w.key0 + (m - w.ns) * kTileKeys;
-  return w.key0 + m * kTileKeys;
 }
 
 __device__ __forceinline__ void gathered_unit(const AttnParams &p, int4 rec, Unit &w) {
@@ -257,7 +241,7 @@ struct UnitIter {
       if (u + (int)gridDim.x < u_end) nxt = __ldg(p.tiles + u + gridDim.x);
       gathered_unit(p, cur, w);
     } else {
-      query_major_unit<MODE>(p, u, w);
+      query_major_unit(p, u, w);
     }
   }
   __device__ __forceinline__ void next() { u += gridDim.x; }
@@ -331,7 +315,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    if (MODE != kGathered || p.q_gather_tma) tma_prefetch_desc(&tmQ);
+    if (MODE == kQueryMajor || p.q_gather_tma) tma_prefetch_desc(&tmQ);
   }
   if (warp == 1) {
     tmem_alloc(&bar.tmem_base, 512);
@@ -368,7 +352,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         for (UnitIter<MODE> it(p, u_begin, u_end); ok && it.valid(); it.next()) {
           Unit w;
           it.get(p, w);
-          if (MODE != kGathered && kside) {
+          if (MODE == kQueryMajor && kside) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               if (!ok) break;
@@ -387,7 +371,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           for (int m = 0; m < w.nc; ++m, ++cnt) {
             const int st = cnt % C::ST;
             if (!(ok = mbar_wait(&empty[st], ((cnt / C::ST) & 1) ^ 1, abort, p.status, site0 + 2))) break;
-            const int key = chunk_key<MODE>(w, m);
+            const int key = w.key0 + m * kTileKeys;
             unsigned char *dst = sbase + off + st * C::TILE;
             if (skip_first && cnt == 0) continue;   // nothing issued, nothing to drain
             mbar_arrive_expect_tx(&full[st], C::BYTES);
@@ -672,7 +656,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         tc_fence_after();
         uint32_t sv[128];
         float *s = reinterpret_cast<float *>(sv);
-        const int key0 = chunk_key<MODE>(w, m);
+        const int key0 = w.key0 + m * kTileKeys;
         float lsum;
         if constexpr (MODE == kGathered) {
           // S of the chunk into registers (the gathered pass has no masks).
@@ -757,17 +741,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           tmem_ld64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(&sv[64]));
           tmem_wait_ld();
           // Masks.
-          if constexpr (MODE == kSinkBand) {
-            const bool full = (key0 + kTileKeys - 1 <= a0) &&
-                              (key0 >= a0 + t.rows - 1 - p.window + 1 || key0 + kTileKeys <= p.sink);
-            if (!full) {
-  #pragma unroll
-              for (int e = 0; e < 128; ++e) {
-                const int j = key0 + e;
-                if (j > pos || (pos - j >= p.window && j >= p.sink)) s[e] = -INFINITY;
-              }
-            }
-          }
           if (MODE == kQueryMajor) {
             if (p.is_moba) {
               if (key0 < cBr) {
@@ -970,12 +943,6 @@ cudaError_t launch_attn(const CUtensorMap *maps, const AttnParams &p, int mode, 
       case 64: return launch_attn_dm<64, kQueryMajor>(maps, p, grid, st);
       case 80: return launch_attn_dm<80, kQueryMajor>(maps, p, grid, st);
       case 128: return launch_attn_dm<128, kQueryMajor>(maps, p, grid, st);
-    }
-  } else if (mode == kSinkBand) {
-    switch (p.d) {
-      case 64: return launch_attn_dm<64, kSinkBand>(maps, p, grid, st);
-      case 80: return launch_attn_dm<80, kSinkBand>(maps, p, grid, st);
-      case 128: return launch_attn_dm<128, kSinkBand>(maps, p, grid, st);
     }
   } else {
     switch (p.d) {

@@ -127,7 +127,6 @@ struct ScatterParams {
 enum AttnMode : int {
   kQueryMajor = 0,  // contiguous 128-row query tiles: own block (MoBA) or band (SWA)
   kGathered = 1,    // gathered rows of one block-major list against one whole block
-  kSinkBand = 2,    // contiguous tiles: band (SWA) and the first keys (sinks)
 };
 
 struct AttnParams {
@@ -142,7 +141,7 @@ struct AttnParams {
   // Problem: N query rows; keys and values run over q_off + N positions, query row i
   // sits at position q_off + i.
   int batch, hq, hkv, N, d, block, topk, window, G;
-  int sink;                // kSinkBand: keys [0, sink) stay visible behind the window
+  int sink;                // swa_fwd.cu: keys [0, sink) stay visible behind the window
   int q_off;
   float scale_log2;        // scale * log2(e)
   int is_moba;             // 0: sliding window only (swa_attn_fwd)

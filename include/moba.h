@@ -348,7 +348,7 @@ int qk_norm_rope_bwd(moba_tensor dq_out, moba_tensor dk_out, moba_tensor q, moba
  *                to the same positions beside them
  *   cosp, sinp, rot, max_pos, interleaved, eps, weights : as in qk_norm_rope_fwd, for k and q;
  *                cosp = sinp = null: no rotation (rot 0)
- * v is copied.  A token whose position is negative, outside the angle table or on a page
+ * v is copied.  Of two tokens with the same place either may stay.  A token whose position is negative, outside the angle table or on a page
  * that is not there ([0, num_pages)) writes nothing and records MOBA_ERR_INDEX.
  */
 int kv_append(moba_tensor k, moba_tensor v, moba_tensor q, const int32_t *cu_seqlens,
@@ -392,7 +392,7 @@ int moba_device_status(void);
  * moba_debug_set_wait_limit_us: every kernel wait that has not completed after this
  *   many microseconds gives up (MOBA_ERR_DEVICE); 0 restores the default of 2 s.
  * moba_debug_fault_next_launch(1): the next attention launch (moba_attn_fwd's passes or
- *   swa_attn_fwd) leaves the first V chunk of its first CTA unloaded, so that a wait
+ *   swa_attn_fwd without sinks) leaves the first V chunk of its first CTA unloaded, so that a wait
  *   runs out on purpose: the launch ends through the bounded-wait path (its roles stop,
  *   copies in flight are drained, TMEM is freed) and moba_device_status() then reports
  *   MOBA_ERR_DEVICE.  One shot: the launch that takes the flag clears it; 0 clears it.

@@ -13,6 +13,10 @@ import torch
 
 BF16, F32 = 2.0 ** -8, 2.0 ** -24
 SLACK = 1.125 + 2.0 ** -8
+# A probability below 2^-126 is flushed to zero, in float32's exponential and in bf16: that
+# moves a dz by at most 2^-126 (|dp| + |D|), and with magnitudes below 2^10 a sum of 2^12
+# products of such dz with q or k by less than 2^-126 2^12 2^10 2^12 = 2^-92.
+FLUSH = 2.0 ** -92
 
 
 def visible(nq, nk, window, sink, device="cpu"):
@@ -32,7 +36,7 @@ def attention(q, k, v, see, scale=None):
     p = torch.where(see, torch.exp(z - torch.nan_to_num(lse, neginf=0.0)[..., None]), 0.0)
     out = p @ v
     # P rounded to bf16 against V, and the stored result.
-    bound = SLACK * BF16 * (out.abs() + p @ v.abs())
+    bound = SLACK * BF16 * (out.abs() + p @ v.abs()) + FLUSH
     # A score is a float32 sum of d products.
     zerr = (q.shape[-1] + 8) * F32 * scale * (q.abs() @ k.abs().transpose(-1, -2)).amax(-1)
     lse_bound = zerr + 2.0 ** -19 * lse.abs().nan_to_num(posinf=0.0).clamp_min(1.0)
@@ -58,7 +62,7 @@ def attention_bwd(q, k, v, do, see, scale=None, out_bound=None):
     slack = 2.0 ** -13 * SLACK
     bq = bq + slack * scale * (p * ((do @ v.transpose(-1, -2)).abs() + dsum.abs())) @ k.abs()
     bk = bk + slack * scale * (p * ((do @ v.transpose(-1, -2)).abs() + dsum.abs())).transpose(-1, -2) @ q.abs()
-    return (dq, bq), (dk, bk), (dv, bv)
+    return (dq, bq + FLUSH), (dk, bk + FLUSH), (dv, bv + FLUSH)
 
 
 def turn(x, cos, sin, interleaved, sign=1.0):

@@ -172,6 +172,67 @@ def test_two_graphs_share_a_workspace():
     assert moba.device_status() == 0
 
 
+def test_pages_beyond_32_bits():
+    """A cache of 2.3 x 10^9 elements: pages at its end, appended to and attended."""
+    moba = _moba()
+    pages, hkv, page, d, n = 140000, 8, 16, 128, 100
+    kp = torch.empty(pages, page, hkv, d, dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+    vp = torch.empty(pages, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    table = (pages - 1 - torch.arange(7, dtype=torch.int32, device="cuda") * 1111)[None].contiguous()
+    table[0, 3] = 0
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    g = torch.Generator("cuda").manual_seed(41)
+    q, k, v = (torch.randn(n, h, d, generator=g, device="cuda").bfloat16() for h in (16, hkv, hkv))
+    moba.kv_append(k, v, kp, vp, table, lens, torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    assert torch.equal(po.gather_pages(kp, table[0], n), k.double().transpose(0, 1))
+    assert torch.equal(po.gather_pages(vp, table[0], n), v.double().transpose(0, 1))
+    out, lse = moba.paged_decode_attn(q[-1:], kp, vp, table, lens)
+    assert moba.device_status() == 0
+    kk, vv = (x.double().transpose(0, 1).repeat_interleave(2, 0) for x in (k, v))
+    o, l, _, ob, lb = po.attention(q[-1].double()[:, None], kk, vv, torch.ones(1, n, dtype=torch.bool, device="cuda"))
+    po.check("out", out[0], o[:, 0], ob[:, 0])
+    po.check("lse", lse[0], l[:, 0], lb[:, 0])
+
+
+def test_shared_pages():
+    """Sequences that share a prefix's pages, and a page named twice in one sequence."""
+    moba = _moba()
+    c, q, out, lse = _decode([64, 64], 4, 2, 16, 64, seed=8)
+    table = c.table.clone()
+    table[1, :3] = table[0, :3]
+    table[1, 3] = table[1, 0]
+    got, gl = moba.paged_decode_attn(q, c.k, c.v, table, c.lens)
+    assert moba.device_status() == 0 and torch.equal(got[0], out[0])
+    k, v = (po.gather_pages(x, table[1], 64).repeat_interleave(2, 0) for x in (c.k, c.v))
+    o, _, _, ob, _ = po.attention(q[1].double()[:, None], k, v, torch.ones(1, 64, dtype=torch.bool, device="cuda"))
+    po.check("out", got[1], o[:, 0], ob[:, 0])
+
+
+def test_the_binding_names_what_is_wrong():
+    moba = _moba()
+    c = Cache([20, 3], 2, 16, 64)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    for match, call in (
+            ("q must be torch.bfloat16", lambda: moba.paged_decode_attn(q.float(), c.k, c.v, c.table, c.lens)),
+            ("seq_lens must be torch.int32", lambda: moba.paged_decode_attn(q, c.k, c.v, c.table, c.lens.long())),
+            ("page_table has shape", lambda: moba.paged_decode_attn(q[:1], c.k, c.v, c.table, c.lens[:1])),
+            ("v_pages has shape", lambda: moba.paged_decode_attn(q, c.k, c.v[:1], c.table, c.lens)),
+            ("k_pages has shape", lambda: moba.paged_decode_attn(q[..., :32], c.k, c.v, c.table, c.lens)),
+            ("page_table must be contiguous", lambda: moba.paged_decode_attn(q, c.k, c.v, c.table.repeat(1, 2)[:, ::2],
+                                                                             c.lens)),
+            ("head dimension", lambda: moba.paged_decode_attn(q.repeat(1, 1, 2)[..., ::2], c.k, c.v, c.table, c.lens)),
+            ("lse must be a CUDA tensor", lambda: moba.paged_decode_attn(q, c.k, c.v, c.table, c.lens,
+                                                                         lse=torch.zeros(2, 4))),
+            ("cos and sin", lambda: moba.kv_append(q[:, :2], q[:, :2], c.k, c.v, c.table, c.lens, cos=torch.zeros(9, 8, device="cuda"))),
+            ("need q", lambda: moba.kv_append(q[:, :2], q[:, :2], c.k, c.v, c.table, c.lens, q_out=q))):
+        with pytest.raises(ValueError, match=match):
+            call()
+    with pytest.raises(moba.MobaError) as e:
+        moba.paged_decode_attn(q, c.k, c.v, c.table, c.lens, window=-2)
+    assert e.value.code == -4
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ append
 
 def _append(news, lens, hq, hkv, page, d, rot, norm, inter, layout="hnd", pad=0, seed=0, cu_null=False):

@@ -96,6 +96,64 @@ def test_backward_of_shared_heads_and_split_sinks(d, batch, hq, hkv, n, window, 
     _bwd(batch, hq, hkv, n, d, window, sink, seed=n, strided=True)
 
 
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("up", [True, False])
+def test_scores_that_climb_or_fall_by_hundreds(d, up):
+    """Keys whose scores rise along the sequence raise the running maximum in every chunk (by
+    far more than 2^8), and falling ones never; probabilities reach one key or many."""
+    moba = _moba()
+    n, window, sink = 1300, 500, 70
+    q, k, v, do = _inputs(1, 2, 1, n, n, d, 21)
+    ramp = torch.linspace(0, 1, n, device="cuda")
+    ramp = ramp if up else 1 - ramp
+    # One direction carries the ramp: 8 x 8 x 60 x d^-0.5, 480 natural units at d = 64.
+    q[..., 0] = 8.0
+    k[..., 0] = (480 * ramp).bfloat16()
+    out, lse = moba.swa_attn_fwd(q, k, v, window, sink=sink)
+    dq, dk, dv = moba.swa_attn_bwd(q, k, v, out, lse, do, window, sink)
+    assert moba.device_status() == 0
+    see = po.visible(n, n, window, sink, "cuda")
+    o, l, p, ob, lb = po.attention(q.double(), _wide(k, 2), _wide(v, 2), see)
+    # Scores of hundreds carry float32 errors of their own size: (d + 8) 2^-24 of the sum of
+    # magnitudes (lb has it) moves every probability by as much, twice in the quotient.
+    move = 2 * lb[..., None]
+    po.check("out", out, o, ob + move * (p @ _wide(v, 2).abs()))
+    po.check("lse", lse, l, lb)
+    (wq, bq), (wk, bk), (wv, bv) = po.attention_bwd(q.double(), _wide(k, 2), _wide(v, 2), do.double(), see, None,
+                                                    ob + move * (p @ _wide(v, 2).abs()))
+    scale = d ** -0.5
+    spread = p * ((do.double() @ _wide(v, 2).mT).abs() + (do.double() * o).sum(-1, keepdim=True).abs()) * move
+    fold = lambda x: x.view(1, 1, 2, n, d).sum(2)  # noqa: E731
+    po.check("dq", dq, wq, bq + scale * spread @ _wide(k, 2).abs())
+    po.check("dk", dk, fold(wk), fold(bk + scale * spread.mT @ q.double().abs()))
+    po.check("dv", dv, fold(wv), fold(bv + (p * move).mT @ do.double().abs()))
+
+
+def test_offsets_beyond_32_bits():
+    """A million positions of 32 heads of 128: 2^32 elements of q and out; the last rows of the
+    last head, and the first's."""
+    moba = _moba()
+    n, d, window, sink = 1 << 20, 128, 128, 3
+    g = torch.Generator("cuda").manual_seed(31)
+    q = torch.empty(1, 32, n, d, dtype=torch.bfloat16, device="cuda")
+    for h in range(32):
+        q[0, h].copy_(torch.randn(n, d, generator=g, device="cuda"))
+    k, v = (torch.randn(1, 2, n, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    out, lse = moba.swa_attn_fwd(q, k, v, window, sink=sink)
+    cos, sin = torch.ones(n, 8, device="cuda"), torch.zeros(n, 8, device="cuda")
+    same, _ = moba.qk_norm_rope_fwd(q, k, cos, sin)
+    assert moba.device_status() == 0
+    assert torch.equal(same[0, 31, -300:], q[0, 31, -300:]) and torch.equal(same[0, 0, :9], q[0, 0, :9])
+    at = torch.cat([torch.arange(sink, device="cuda"), torch.arange(n - 400, n, device="cuda")])
+    see = torch.cat([torch.ones(200, sink, dtype=torch.bool, device="cuda"),
+                     po.visible(200, 400, window, 0, "cuda")], 1)
+    for h in (0, 15, 31):
+        kk, vv = k[0, h // 16, at].double(), v[0, h // 16, at].double()
+        o, l, _, ob, lb = po.attention(q[0, h, -200:].double(), kk, vv, see)
+        po.check("out", out[0, h, -200:], o, ob)
+        po.check("lse", lse[0, h, -200:], l, lb)
+
+
 def test_backward_with_a_scale_repeats_bit_for_bit():
     moba = _moba()
     (q, k, v, do, out, lse), grads = _bwd(1, 4, 2, 1500, 64, 90, 7, scale=0.3)
