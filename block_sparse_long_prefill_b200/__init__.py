@@ -1,10 +1,12 @@
-"""MoBA block-sparse attention prefill and sliding-window attention prefill on B200.
+"""MoBA block-sparse attention prefill and sliding-window attention prefill on B200, with
+the operators around them: sinks and the backward of the sliding window, norms per head
+with the rotary embedding, and a paged key-value cache with its append and its decode.
 
-A thin ctypes binding over ``libmoba.so`` (declared in ``include/moba.h``).  The
+A thin binding over ``libmoba.so`` (declared in ``include/moba.h``): ctypes, and a compiled
+module (``_binding``) for the calls that take about as long on the host as on the GPU.  The
 functions here only turn torch tensors into pointers, strides and a stream and pass
 them through the C ABI: every step of the computation runs in the library's sm_100a
-kernels.  There is no CPU fallback; importing fails loudly when the library is
-missing.
+kernels.  There is no CPU fallback; importing fails loudly when either is missing.
 
 Method sources (by page title and section):
   [MoBA] "MoBA: 어텐션에 전문가 혼합을 적용해 긴 문맥을 효율적으로 처리하는 블록 어텐션

@@ -13,7 +13,9 @@
 // (normalised rows and their log-sum-exp) that a second, small kernel joins.  An item counts
 // as its tiles and kDecItem more, about what filling the pipeline and joining the warps
 // costs: by tiles alone a run of many one-tile items took six times as long as one of few
-// long items.
+// long items (32 ragged sequences of 32 heads with a window of 4096: 237 against 88 us).
+// Measured: one sequence of 2^20 tokens, 8 KV heads of 128, 683 us with the call, 6.3 TB/s;
+// 48 ragged sequences of up to 16384 tokens 90 us, 5.1 TB/s (fills and ends of 384 items).
 //
 // A warp takes every fourth tile of its CTA's run and works alone: its tiles arrive by
 // cp.async in a ring of its own (three stages of 16 keys and 16 values, about 9 KB each,
