@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
           const Vec8 x = unpack_v(from[(R + i) * 32]), gw = mul_v(g, w);
           const float ss = row_sum<D>(dot_v(x, x), base, vv);
           const float gx = row_sum<D>(dot_v(gw, x), base, vv);
-          const float r = rsqrtf(ss * (1.f / D) + p.eps);
+          // (A lane without a row has zeros, which eps = 0 would turn into 0 times infinity.)
+          const float r = cur.live ? rsqrtf(ss * (1.f / D) + p.eps) : 0.f;
           const Vec8 xn = mul_v(x, r);
           dw = fma_v(g, xn, dw);
           const float m = -gx * (1.f / D) * r;

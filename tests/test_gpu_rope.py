@@ -134,6 +134,26 @@ def test_positions_outside_the_table_are_left_out():
     assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
 
 
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_without_an_epsilon(d):
+    """eps = 0 is allowed; lanes without a row (n no multiple of a warp's rows, positions out of
+    range) must not leave 0 / 0 in the weights' gradients."""
+    moba = _moba()
+    q, k, cos, sin, pos, w, (c, s), rand = _case(2, 3, 1, 13, d, 32, "f32", True, seed=d)
+    gq, gk = rand(*q.shape).bfloat16(), rand(*k.shape).bfloat16()
+    qo, ko = moba.qk_norm_rope_fwd(q, k, cos, sin, pos, *w, 0.0)
+    po.check("q", qo, *po.norm_rope(q.double(), w[0].double(), c, s, False, 0.0))
+    got = moba.qk_norm_rope_bwd(gq, gk, q, k, cos, sin, pos, *w, 0.0)
+    for name, g, x, dx, wt, dw in (("q", gq, q, got[0], w[0], got[2]), ("k", gk, k, got[1], w[1], got[3])):
+        want, wdw = po.norm_rope_bwd(g.double(), x.double(), wt.double(), c, s, False, 0.0)
+        po.check("d" + name, dx, *want)
+        po.check("dw" + name, dw, *wdw)
+    pos[0, 5] = -1
+    got = moba.qk_norm_rope_bwd(gq, gk, q, k, cos, sin, pos, *w, 0.0)
+    assert moba.device_status() == -10
+    assert torch.isfinite(got[2]).all() and torch.isfinite(got[3]).all()
+
+
 def test_in_a_graph_and_on_another_stream():
     moba = _moba()
     q, k, cos, sin, pos, w, _, rand = _case(1, 8, 2, 300, 128, 128, "bf16", True)
