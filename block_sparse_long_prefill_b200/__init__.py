@@ -194,6 +194,15 @@ def _on_stream(stream):
     return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
+def _hand_over(stream, *results):
+    """Results allocated on ``stream`` go to a caller on the current stream, which may drop
+    them with work of its own still to come."""
+    if stream is not None:
+        for t in results:
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def workspace_size(batch, hq, hkv, N, d, block, topk) -> int:
     out = ctypes.c_size_t(0)
     _check("moba_workspace_size",
@@ -303,6 +312,7 @@ def swa_attn_fwd_chunk(q, k, v, window: int, scale: float = 0.0, out=None, lse=N
     with _on_stream(stream):
         rc, out, lse = _binding.swa_fwd(q, k, v, window, sink, scale, out, lse)
     _check("swa_attn_fwd", rc)
+    _hand_over(stream, out, lse)
     return out, lse
 
 
@@ -321,6 +331,7 @@ def swa_attn_bwd(q, k, v, out, lse, dout, window: int, sink: int = 0, scale: flo
     with _on_stream(stream):
         rc, dq, dk, dv = _binding.swa_bwd(q, k, v, out, lse, dout, window, sink, scale, dq, dk, dv, workspace)
     _check("swa_attn_bwd", rc)
+    _hand_over(stream, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -335,6 +346,7 @@ def qk_norm_rope_fwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=Non
         rc, q_out, k_out = _binding.rope_fwd(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved,
                                              q_out, k_out)
     _check("qk_norm_rope_fwd", rc)
+    _hand_over(stream, q_out, k_out)
     return q_out, k_out
 
 
@@ -348,6 +360,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=No
         rc, dq, dk, dq_weight, dk_weight = _binding.rope_bwd(dq_out, dk_out, q, k, cos, sin, positions, q_weight,
                                                              k_weight, eps, interleaved, dq, dk, workspace)
     _check("qk_norm_rope_bwd", rc)
+    _hand_over(stream, dq, dk, dq_weight, dk_weight)
     return dq, dk, dq_weight, dk_weight
 
 
@@ -366,6 +379,7 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos
         rc, q_out = _binding.append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, cos, sin, k_weight,
                                     eps, interleaved, q, q_weight, q_out)
     _check("kv_append", rc)
+    _hand_over(stream, q_out)
     return q_out
 
 
@@ -387,6 +401,7 @@ def paged_decode_attn(q, k_pages, v_pages, page_table, seq_lens, window: int = 0
         rc, out, lse = _binding.decode(q, k_pages, v_pages, page_table, seq_lens, window, sink, scale, out, lse,
                                        workspace)
     _check("paged_decode_attn", rc)
+    _hand_over(stream, out, lse)
     return out, lse
 
 

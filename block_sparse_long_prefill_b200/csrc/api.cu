@@ -223,12 +223,14 @@ int check_weights(const moba_weight &q, const moba_weight &k, float eps) {
   return eps >= 0.f ? MOBA_OK : MOBA_ERR_ARG;   // (false for NaN)
 }
 
+// Groups of rows are counted in 32 bits, and as blocks of one grid dimension.
+bool rope_rows(int batch, int N, double heads) { return (double)batch * N * heads < 8589934592.0; }
+
 int check_rope(const float *cosp, const float *sinp, const int32_t *positions, const moba_weight &qw,
                const moba_weight &kw, int batch, int hq, int hkv, int N, int d, int rot, int max_pos,
                int interleaved, float eps) {
   if (batch < 1 || hq < 1 || hkv < 1 || N < 1 || max_pos < 1) return MOBA_ERR_SHAPE;
-  // Groups of rows are counted in 32 bits, and as blocks of one grid dimension.
-  if ((double)batch * N * ((double)hq + hkv) >= 8589934592.0) return MOBA_ERR_SHAPE;
+  if (!rope_rows(batch, N, (double)hq + hkv)) return MOBA_ERR_SHAPE;
   int rc = check_attn_dim(d);
   if (rc) return rc;
   if (rot < 16 || rot > d || rot % 16) return MOBA_ERR_DIM;
@@ -584,6 +586,8 @@ int swa_sink_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, in
   // Query row i sits at key position Nk - N + i (any offset).
   const int q_off = Nk - N;
   if (q_off < 0 || (long long)Nk >= (1ll << 31)) return MOBA_ERR_SHAPE;
+  // (With sinks, positions of a whole tile and of its keys are counted in 32 bits.)
+  if (sink > 0 && Nk > 0x7fffffff - 512) return MOBA_ERR_SHAPE;
   if (window < 1 || sink < 0) return MOBA_ERR_ARG;
   int rc = check_attn_dim(d);
   if (rc) return rc;
@@ -725,6 +729,9 @@ int swa_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, m
   if (!writable(dq, batch, hq, N) || !writable(dk, batch, hkv, N) || !writable(dv, batch, hkv, N))
     return MOBA_ERR_ARG;
   if (!lse) return MOBA_ERR_ARG;
+  // (The kernels hold lse / scale.)
+  const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
+  if (sc < 1e-30f) return MOBA_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOBA_ERR_ALIGN;
   const int w = window < N ? window : N;
   const SwaBwdPlan plan = swa_bwd_plan(batch, hq, hkv, N, d, w, sink);
@@ -758,7 +765,6 @@ int swa_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, m
   p.sink = sink < N ? sink : N;
   p.G = hq / hkv;
   p.nt = plan.nt; p.nst = plan.nst; p.seg = plan.seg; p.nseg = plan.nseg;
-  const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
   p.scale = sc;
   p.scale_log2 = sc * 1.4426950408889634f;
   return launch_status(launch_swa_bwd(maps, p, nsm, static_cast<cudaStream_t>(stream)));
@@ -791,7 +797,7 @@ int qk_norm_rope_fwd(moba_tensor q, moba_tensor k, const float *cosp, const floa
 
 int qk_norm_rope_bwd_workspace_size(int batch, int hq, int hkv, int N, int d, size_t *bytes) {
   if (!bytes) return MOBA_ERR_ARG;
-  if (batch < 1 || hq < 1 || hkv < 1 || N < 1) return MOBA_ERR_SHAPE;
+  if (batch < 1 || hq < 1 || hkv < 1 || N < 1 || !rope_rows(batch, N, (double)hq + hkv)) return MOBA_ERR_SHAPE;
   const int rc = check_attn_dim(d);
   if (rc) return rc;
   *bytes = size_t(rope_bwd_ctas(batch, hq, hkv, N, d)) * 2 * d * sizeof(float);
@@ -846,6 +852,7 @@ int kv_append(moba_tensor k, moba_tensor v, moba_tensor q, const int32_t *cu_seq
               int num_pages, int max_pages, moba_tensor k_pages, moba_tensor v_pages,
               moba_tensor q_out, void *stream) {
   if (T < 0 || hkv < 1 || (q.ptr && hq < 1)) return MOBA_ERR_SHAPE;
+  if (!rope_rows(1, T, (q.ptr ? (double)hq : 0.0) + 2.0 * hkv)) return MOBA_ERR_SHAPE;
   int rc = check_pages(k_pages, v_pages, page_table, seq_lens, batch, hkv, page, num_pages, max_pages);
   if (rc) return rc;
   if (!cu_seqlens && T != batch) return MOBA_ERR_SHAPE;

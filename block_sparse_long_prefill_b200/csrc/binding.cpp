@@ -40,6 +40,8 @@ class Checks {
 
   void rank(const char *name, const Tensor &t, int64_t n) const {
     if (t.dim() != n) fail(std::string(name) + " has " + std::to_string(t.dim()) + " dimensions, expected " + std::to_string(n));
+    for (int64_t i = 0; i < n; ++i)   // (the C ABI counts in int; an expanded tensor can be longer)
+      if (t.size(i) >= (int64_t(1) << 31)) fail(std::string(name) + " has shape " + show(t.sizes()) + ", beyond 32 bits");
   }
 
   // dt: the type, or at::ScalarType::Undefined for any.  shape null: any.

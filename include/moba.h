@@ -268,8 +268,10 @@ int swa_sink_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, in
  *     D_i = dO_i . o_i,  dz_ij = p_ij (dO_i . v_j - D_i),
  *     dQ_i = scale sum_j dz_ij k_j,  dK_j = scale sum_i dz_ij q_i,  dV_j = sum_i p_ij dO_i
  * (a KV head's dK and dV sum over the q-heads that read it).  d in {64, 80, 128}; any N.
- *   q, k, v, out, lse : as given to / returned by the forward
- *   dout       : bf16 upstream gradient [batch, hq, N, d]
+ *   q, k, v, out, lse : as given to / returned by the forward (scale at least 1e-30,
+ *                MOBA_ERR_ARG otherwise)
+ *   dout       : bf16 upstream gradient [batch, hq, N, d].  q, k, v and dout must be finite
+ *                (masked pairs are multiplied by zero).
  *   dq         : bf16 out [batch, hq, N, d];  dk, dv : bf16 out [batch, hkv, N, d]
  *   workspace  : device buffer of at least swa_bwd_workspace_size() bytes (row statistics,
  *                and partial dK, dV of the sinks)
@@ -348,8 +350,9 @@ int qk_norm_rope_bwd(moba_tensor dq_out, moba_tensor dk_out, moba_tensor q, moba
  *                to the same positions beside them
  *   cosp, sinp, rot, max_pos, interleaved, eps, weights : as in qk_norm_rope_fwd, for k and q;
  *                cosp = sinp = null: no rotation (rot 0)
- * v is copied.  Of two tokens with the same place either may stay.  A token whose position is negative, outside the angle table or on a page
- * that is not there ([0, num_pages)) writes nothing and records MOBA_ERR_INDEX.
+ * v is copied.  Two tokens with the same place (a page that two sequences extend) leave a row
+ * that may hold parts of both.  A token whose position is negative, outside the angle table or
+ * on a page that is not there ([0, num_pages)) writes nothing and records MOBA_ERR_INDEX.
  */
 int kv_append(moba_tensor k, moba_tensor v, moba_tensor q, const int32_t *cu_seqlens,
               const int32_t *seq_lens, const int32_t *page_table, const float *cosp,

@@ -207,3 +207,23 @@ def test_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, o3) and all(torch.equal(a, b) for a, b in zip(want, got))
     assert moba.device_status() == 0
+
+
+def test_results_of_another_stream_stay_until_they_are_read():
+    """A result allocated on the call's stream is read on the caller's behind a long kernel
+    and dropped before that: its memory must not be handed out again meanwhile."""
+    moba = _moba()
+    q, k, v, _ = _inputs(1, 8, 8, 2000, 2000, 128, 9)
+    want, _ = moba.swa_attn_fwd(q, k, v, 100, sink=5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, _ = moba.swa_attn_fwd(q, k, v, 100, sink=5, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(50_000_000)
+    got = torch.empty_like(out)
+    got.copy_(out)
+    del out
+    with torch.cuda.stream(side):
+        junk = [torch.full_like(q, 9.0) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(junk) == 4

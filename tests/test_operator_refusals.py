@@ -24,6 +24,21 @@ def _fwd(q=OK, out=OK, lse=P, batch=1, hq=2, hkv=1, N=100, Nk=200, d=128, window
     return moba.library().swa_sink_attn_fwd(q, OK, OK, batch, hq, hkv, N, Nk, d, window, sink, 0.0, out, lse, None)
 
 
+def test_rows_beyond_32_bits_are_refused():
+    size = ctypes.c_size_t(0)
+    lib = moba.library()
+    assert lib.qk_norm_rope_bwd_workspace_size(1 << 20, 32, 32, 1 << 20, 128, ctypes.byref(size)) == SHAPE
+    assert _append(T_=1 << 30, hkv=8) == SHAPE
+    assert _fwd(Nk=(1 << 31) - 1) == SHAPE
+
+
+@pytest.mark.parametrize("scale", [1e-31, 1e-45])
+def test_backward_of_a_vanishing_scale(scale):
+    """The kernels hold lse / scale in float32."""
+    args = (OK, OK, OK, OK, OK, P, 1, 2, 1, 300, 128, 10, 4)
+    assert moba.library().swa_attn_bwd(*args, scale, OK, OK, OK, P, 1 << 40, None) == ARG
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(sink=-1), ARG), (dict(window=0), ARG), (dict(d=96), DIM), (dict(hq=3, hkv=2), SHAPE), (dict(Nk=99), SHAPE),
     (dict(N=0), SHAPE), (dict(q=NULL), ARG), (dict(q=MIS), ALIGN), (dict(out=ODD), ALIGN), (dict(lse=None), ARG),
