@@ -10,26 +10,31 @@
 //
 // A softmax is a chain (scores to registers, maximum, exponentials, write-back, product),
 // and a chain that must end before its next scores can be issued leaves both the tensor core
-// and the exponential unit idle.  So a chunk is split by keys between two streams of four
-// warps, 64 keys each, that share nothing but the query tile: a stream has its own running
-// maximum and sum, its own accumulator, and two buffers for its scores, so that the next
-// scores are there when it has written its probabilities.  The two partial results of a row
-// are joined when the item is read out, behind the first chunk of the next item.  (The two
-// streams of attn.cu are query tiles of 128 keys; their scores and accumulators fill TMEM
-// with one buffer each.)
+// and the exponential unit idle.  So a chunk is split by keys between groups of four warps
+// that share nothing but the query tile: a group has its own running maximum and sum and its
+// own accumulator, and the next scores are there when it has written its probabilities.  The
+// partial results of a row are joined when the item is read out, behind the first chunk of
+// the next item.  (The two streams of attn.cu are query tiles of 128 keys; their scores and
+// accumulators fill TMEM with one buffer each.)
+//   D = 64, 80  four groups of 32 keys; scores in a ring of three slots of 64 columns beside
+//               the four accumulators.  A warp of 64 keys leaves the exponential unit idle
+//               while it reads, finds the maximum and writes back: two groups took 793 us
+//               below, four 735.
+//   D = 128     two groups of 64 keys, two slots each (more accumulators do not fit).
 //
 // Per 128 x 128 keys 16384 exponentials at 16 a cycle are 1024 cycles; the products are 827
 // cycles at D = 80 and 1291 at D = 128 (64-key products are fed by shared memory: 48 cycles
 // instead of 32).
-// Measured (32 heads, d = 80, N = 16384, window 4096, 4 sinks): 797 us, 755 TFLOP/s at a
+// Measured (32 heads, d = 80, N = 16384, window 4096, 4 sinks): 735 us, 820 TFLOP/s at a
 // power-capped 1.4-1.6 GHz, against 811 us with the two streams over query tiles; one
-// 1000-token prompt (4 heads) 10.6 against 16.7 us in a graph, since a walk's chain is half
+// 1000-token prompt (4 heads) 10.5 against 16.7 us in a graph, since a walk's chain is half
 // as long.
+//
 //   warp 0      TMA: K and V
 //   warp 1      issues S = Q K^T (TMEM owner)
 //   warp 2      issues O += P V
 //   warp 3      TMA: Q
-//   warps 4-11  streams 0 and 1; a thread owns one TMEM lane, a row
+//   warps 4-    the groups; a thread owns one TMEM lane, a row
 // Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -72,25 +77,30 @@ __device__ __forceinline__ int swa_key(const SwaItem &w, int m) {
 
 template <int D>
 struct SwaFwdCfg {
+  static constexpr int GRP = D == 128 ? 2 : 4;                 // softmax groups
+  static constexpr int W = 128 / GRP;                          // keys of a group
+  static constexpr int THREADS = 128 + 128 * GRP;
   static constexpr int QS = 2;                                 // Q stages
   static constexpr int NK = D == 128 ? 2 : 4;                  // K and V stages
   static constexpr int NV = D == 128 ? 2 : 4;
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = QS * SwaTile<D>::TILE;
   static constexpr int V_OFF = K_OFF + NK * SwaTile<D>::TILE;
-  static constexpr int ML_OFF = V_OFF + NV * SwaTile<D>::TILE; // [item parity][stream][128] (m, l)
-  static constexpr int BAR_OFF = ML_OFF + 2 * 2 * 128 * 8;
+  static constexpr int ML_OFF = V_OFF + NV * SwaTile<D>::TILE; // [item parity][group][128] (m, l)
+  static constexpr int BAR_OFF = ML_OFF + 2 * GRP * 128 * 8;
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
-  // TMEM: stream x's scores at 128 x and 128 x + 64 (P is written back over them), its
-  // accumulator.
-  static constexpr uint32_t O = 256;
-  static_assert(O + 2 * D <= 512, "TMEM columns");
+  // TMEM: a ring of 64-column slots for the halves' scores (P is written back over them),
+  // then the groups' accumulators.
+  static constexpr int S = D == 128 ? 4 : 3;
+  static constexpr uint32_t O = 64 * S;
+  static_assert(O + GRP * D <= 512, "TMEM columns");
+  static __device__ __forceinline__ uint32_t s_at(uint32_t h) { return 64 * (h % S); }
 };
 
 struct SwaFwdBars {
   uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // per stream, of even and odd chunks
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // per half, of even and odd chunks
   uint64_t o_full, o_empty, ml_full;
   uint64_t mma_done[2];
   uint32_t tmem_base;
@@ -98,7 +108,7 @@ struct SwaFwdBars {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kSwaThreads, 1)
+__global__ void __launch_bounds__(SwaFwdCfg<D>::THREADS, 1)
 swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK1,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmV1,
@@ -129,12 +139,12 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int x = 0; x < 2; ++x)
       for (int s = 0; s < 2; ++s) {
         mbar_init(&bar.s_full[x][s], 1);
-        mbar_init(&bar.p_full[x][s], 4);     // (a warp arrives once)
+        mbar_init(&bar.p_full[x][s], 2 * C::GRP);   // (a warp arrives once)
         mbar_init(&bar.pv_done[x][s], 1);
       }
     mbar_init(&bar.o_full, 1);
-    mbar_init(&bar.o_empty, 8);
-    mbar_init(&bar.ml_full, 8);
+    mbar_init(&bar.o_empty, 4 * C::GRP);
+    mbar_init(&bar.ml_full, 4 * C::GRP);
     mbar_init(&bar.mma_done[0], 1);
     mbar_init(&bar.mma_done[1], 1);
     bar.abort = 0;
@@ -200,7 +210,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S
-    // Of each chunk and stream, once the buffer's last probabilities have been consumed.
+    // Of each half chunk, once its slot's last probabilities have been consumed.
     uint32_t step = 0, qn = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++qn) {
@@ -208,15 +218,19 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const uint32_t qs = qn % C::QS, qt = base + C::Q_OFF + qs * T::TILE;
       if (!(ok = mbar_wait_warp(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
       for (int m = 0; ok && m < w.nc; ++m, ++step) {
-        const uint32_t ks = step % C::NK, kt = base + C::K_OFF + ks * T::TILE, sl = step & 1;
+        const uint32_t ks = step % C::NK, kt = base + C::K_OFF + ks * T::TILE;
         if (!(ok = mbar_wait_warp(&bar.k_full[ks], (step / C::NK) & 1, abort, p.status, site0 + 4))) break;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (!(ok = mbar_wait_warp(&bar.pv_done[x][sl], ((step >> 1) & 1) ^ 1, abort, p.status, site0 + 5))) break;
+          // The half that had the slot before, h - S: its chunk and half.
+          const uint32_t h = 2 * step + x, chunk = (h - C::S) >> 1;
+          if (h >= C::S && !(ok = mbar_wait_warp(&bar.pv_done[(h - C::S) & 1][chunk & 1], (chunk >> 1) & 1, abort,
+                                                 p.status, site0 + 5)))
+            break;
           tc_fence_after();
           if (elect_one()) {
-            swa_scores<D, 64>(tmem + 128 * x + 64 * sl, qt, kt, 64 * x);
-            umma_commit(&bar.s_full[x][sl]);
+            swa_scores<D, 64>(tmem + C::s_at(h), qt, kt, 64 * x);
+            umma_commit(&bar.s_full[x][step & 1]);
             if (x == 1) {
               umma_commit(&bar.k_empty[ks]);
               if (m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
@@ -242,7 +256,13 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           if (m == 0 && x == 0 && !(ok = mbar_wait_warp(&bar.o_empty, (an & 1) ^ 1, abort, p.status, site0 + 8))) break;
           tc_fence_after();
           if (elect_one()) {
-            swa_acc<D>(tmem + C::O + D * x, tmem + 128 * x + 64 * sl, vt, x, m == 0);
+            const uint32_t tP = tmem + C::s_at(2 * step + x);
+            if constexpr (C::GRP == 2) {
+              swa_acc<D>(tmem + C::O + D * x, tP, vt, x, m == 0);
+            } else {
+              swa_acc32<D>(tmem + C::O + D * (2 * x), tP, vt, 2 * x, m == 0);
+              swa_acc32<D>(tmem + C::O + D * (2 * x + 1), tP + 32, vt, 2 * x + 1, m == 0);
+            }
             umma_commit(&bar.pv_done[x][sl]);
             if (x == 1) {
               umma_commit(&bar.v_empty[vs]);
@@ -256,10 +276,11 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     swa_issued(&bar.mma_done[1], p.status);
   } else {
     // ------------------------------------------------------------ softmax, and O out
-    const int q4 = warp & 3, x = (warp - 4) >> 2;
+    const int q4 = warp & 3, grp = (warp - 4) >> 2;
+    const int x = grp * 2 / C::GRP, sub = grp * C::W - 64 * x;   // half, first column there
     const int r = 32 * q4 + lane;                   // row == TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    const uint32_t tO = tmem + lane_off + C::O;
+    const uint32_t tO = tmem + lane_off + C::O, tOg = tO + D * grp;
     float2 *ml = reinterpret_cast<float2 *>(sbase + C::ML_OFF);
     const float sl2 = p.scale_log2;
     uint32_t sc = 0, an = 0;                        // chunks, items read out
@@ -270,28 +291,44 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (!mbar_wait_warp(&bar.ml_full, an & 1, abort, p.status, site0 + 9)) return false;
       if (!mbar_wait_warp(&bar.o_full, an & 1, abort, p.status, site0 + 10)) return false;
       tc_fence_after();
-      const float2 a = ml[(an & 1) * 256 + r], b = ml[(an & 1) * 256 + 128 + r];
+      float wgt[C::GRP], mx = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int g = 0; g < C::GRP; ++g) mx = fmaxf(mx, ml[((an & 1) * C::GRP + g) * 128 + r].x);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+      for (int g = 0; g < C::GRP; ++g) {
+        const float2 a = ml[((an & 1) * C::GRP + g) * 128 + r];
+        wgt[g] = ex2_approx(a.x - mu);
+        l = fmaf(wgt[g], a.y, l);
+      }
       ++an;
-      const float mx = fmaxf(a.x, b.x), mu = mx == -INFINITY ? 0.f : mx;
-      const float fa = ex2_approx(a.x - mu), fb = ex2_approx(b.x - mu);
-      const float l = fmaf(fa, a.y, fb * b.y), inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-      const float wa = fa * inv, wb = fb * inv;
-      constexpr int CUT = D == 80 ? 48 : D / 2;     // columns that stream 0 writes
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+      for (int g = 0; g < C::GRP; ++g) wgt[g] *= inv;
 #pragma unroll
       for (int c = 0; c < D; c += 16) {
-        if ((c < CUT) != (x == 0)) continue;
-        uint32_t u[16], v[16];
-        tmem_ld16(tO + c, u);
-        tmem_ld16(tO + D + c, v);
-        tmem_wait_ld();
-        if (live) {
+        if (c / 16 % C::GRP != grp) continue;
+        float o[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            u[e] = __float_as_uint(fmaf(wa, __uint_as_float(u[e]), wb * __uint_as_float(v[e])));
-          store16(dst + c, u, 1.f);                 // one whole 32-byte sector of the row
+        for (int g = 0; g < C::GRP; g += 2) {
+          uint32_t u[16], v[16];
+          tmem_ld16(tO + D * g + c, u);
+          tmem_ld16(tO + D * (g + 1) + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float t = g == 0 ? wgt[0] * __uint_as_float(u[e]) : fmaf(wgt[g], __uint_as_float(u[e]), o[e]);
+            o[e] = fmaf(wgt[g + 1], __uint_as_float(v[e]), t);
+          }
+        }
+        if (live) {                                 // one whole 32-byte sector of the row
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e]);
+          store16(dst + c, u, 1.f);
         }
       }
-      if (live && x == 0) *ldst = (mu + log2f(l)) * 0.69314718055994530942f;
+      if (live && grp == 0) *ldst = (mu + log2f(l)) * 0.69314718055994530942f;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.o_empty);
@@ -306,16 +343,17 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const uint32_t sl = sc & 1;
         if (!(ok = mbar_wait_warp(&bar.s_full[x][sl], (sc >> 1) & 1, abort, p.status, site0 + 11))) break;
         tc_fence_after();
-        const int key0 = swa_key(w, m) + 64 * x;
-        const bool full = key0 + 63 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + 64 <= p.sink);
-        const uint32_t tS = tmem + lane_off + 128 * x + 64 * sl;
-        uint32_t sv[64];
+        const int key0 = swa_key(w, m) + C::W * grp;
+        const bool full = key0 + C::W - 1 <= i0 && (i0 + kTileRows - 1 - key0 < p.window || key0 + C::W <= p.sink);
+        const uint32_t tS = tmem + lane_off + C::s_at(2 * sc + x) + sub;
+        uint32_t sv[C::W];
         float *s = reinterpret_cast<float *>(sv);
-        tmem_ld64(tS, sv);
+        if constexpr (C::W == 64) tmem_ld64(tS, sv);
+        else tmem_ld32(tS, sv);
         tmem_wait_ld();
         if (!full) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
+          for (int c = 0; c < C::W; c += 32) {
             const uint32_t b = first_bits(pos + 1 - key0 - c) &
                                (~first_bits(pos + 1 - p.window - key0 - c) | first_bits(p.sink - key0 - c));
 #pragma unroll
@@ -325,7 +363,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 4; e < 64; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], s[e]);
+        for (int e = 4; e < C::W; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], s[e]);
         const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2);
         const bool raise = m_new > m_run + kSwaRaise;        // (from -inf too)
         if (__any_sync(FULL, raise)) {
@@ -341,18 +379,18 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
               uint32_t o[16];
-              tmem_ld16(tO + D * x + c, o);
+              tmem_ld16(tOg + c, o);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st16(tO + D * x + c, o);
+              tmem_st16(tOg + c, o);
             }
           }
         }
         const float mu = m_run == -INFINITY ? 0.f : m_run;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
+        for (int c = 0; c < C::W; c += 32) {
           uint32_t pp[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -376,7 +414,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
       }
       if (!ok) break;
-      ml[(in & 1) * 256 + 128 * x + r] = make_float2(m_run, l_run);
+      ml[((in & 1) * C::GRP + grp) * 128 + r] = make_float2(m_run, l_run);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ml_full);
       const int i = w.qt * kTileRows + r;
@@ -401,7 +439,7 @@ template <int D>
 static cudaError_t launch_swa_fwd_d(const CUtensorMap *m, const AttnParams &p, int nsm, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(swa_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SwaFwdCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  swa_fwd_kernel<D><<<p.ntiles < nsm ? p.ntiles : nsm, kSwaThreads, SwaFwdCfg<D>::SMEM, st>>>(
+  swa_fwd_kernel<D><<<p.ntiles < nsm ? p.ntiles : nsm, SwaFwdCfg<D>::THREADS, SwaFwdCfg<D>::SMEM, st>>>(
       m[0], m[1], m[2], m[3], m[4], m[5], p);
   return cudaGetLastError();
 }

@@ -10,8 +10,6 @@
 
 namespace moba {
 
-constexpr int kSwaThreads = 384;
-
 // A 128-row tile of D columns: a 64-column region with 128-byte swizzle, then columns
 // [64, 128) the same way (D = 128) or [64, 80) with 32-byte swizzle (D = 80).
 template <int D>
@@ -39,6 +37,19 @@ __device__ __forceinline__ void swa_acc(uint32_t d, uint32_t a, uint32_t tile, i
     const uint32_t acc = (kk == 0 && fresh) ? 0u : 1u;
     umma_ts_w(d, a + kk * 8 + (kk >> 1) * GAP, b + kk * 128, kHi128, idesc_bf16(128, D == 128 ? 128 : 64, 0, 1), acc);
     if (D == 80) umma_ts_w(d + 64, a + kk * 8 + (kk >> 1) * GAP, b1 + kk * 32, kHi32, idesc_bf16(128, 16, 0, 1), acc);
+  }
+}
+
+// The same over the 32 rows from 32 quarter on: two steps.
+template <int D>
+__device__ __forceinline__ void swa_acc32(uint32_t d, uint32_t a, uint32_t tile, int quarter, bool fresh) {
+  const uint32_t b = desc_lo(tile, D == 128 ? SwaTile<D>::R0 : 16) + quarter * 256;
+  const uint32_t b1 = desc_lo(tile + SwaTile<D>::R0, 16) + quarter * 64;
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    const uint32_t acc = (kk == 0 && fresh) ? 0u : 1u;
+    umma_ts_w(d, a + kk * 8, b + kk * 128, kHi128, idesc_bf16(128, D == 128 ? 128 : 64, 0, 1), acc);
+    if (D == 80) umma_ts_w(d + 64, a + kk * 8, b1 + kk * 32, kHi32, idesc_bf16(128, 16, 0, 1), acc);
   }
 }
 
