@@ -16,11 +16,16 @@
 // partial results of a row are joined when the item is read out, behind the first chunk of
 // the next item.  (The two streams of attn.cu are query tiles of 128 keys; their scores and
 // accumulators fill TMEM with one buffer each.)
-//   D = 64, 80  four groups of 32 keys; scores in a ring of three slots of 64 columns beside
-//               the four accumulators.  A warp of 64 keys leaves the exponential unit idle
+//   D = 64, 80  four groups of 32 keys.  A warp of 64 keys leaves the exponential unit idle
 //               while it reads, finds the maximum and writes back: two groups took 793 us
 //               below, four 735.
-//   D = 128     two groups of 64 keys, two slots each (more accumulators do not fit).
+//   D = 128     two groups of 64 keys (more accumulators do not fit).  Four groups in pairs
+//               that exchange their maxima took 475 against 458 us (16 heads over 4, 16384
+//               tokens, window 4096), and 869 us below.
+// The halves' scores stand in a ring of three slots of 64 columns: a half's next scores wait
+// for the other half's last product, which keeps the halves apart, so that one reads and
+// writes while the other uses the exponential unit (four slots: 112.8 against 106.5 us at
+// D = 64, 8192 tokens, window 2048; 461 against 457 us at D = 128 as above).
 //
 // Per 128 x 128 keys 16384 exponentials at 16 a cycle are 1024 cycles; the products are 827
 // cycles at D = 80 and 1291 at D = 128 (64-key products are fed by shared memory: 48 cycles
@@ -92,7 +97,7 @@ struct SwaFwdCfg {
   static_assert(SMEM <= 232448, "shared memory of a CTA");
   // TMEM: a ring of 64-column slots for the halves' scores (P is written back over them),
   // then the groups' accumulators.
-  static constexpr int S = D == 128 ? 4 : 3;
+  static constexpr int S = 3;
   static constexpr uint32_t O = 64 * S;
   static_assert(O + GRP * D <= 512, "TMEM columns");
   static __device__ __forceinline__ uint32_t s_at(uint32_t h) { return 64 * (h % S); }
