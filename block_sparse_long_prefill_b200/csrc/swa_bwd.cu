@@ -34,7 +34,7 @@
 // Measured (batch 1, 32 heads, d = 80, N = 16384, window 4096, 4 sinks): statistics 51 us
 // (3.7 TB/s), dQ 855 us (1056 TFLOP/s over its 3 products), dK and dV 1028 us (1171 TFLOP/s
 // over 4), parts 5 us, at a power-capped 1.3-1.6 GHz; a tile takes 1892 and 2270 cycles.  8192 tokens, 8
-// heads over 4, d = 128, window 512, 130 sinks: 11, 48, 90 and 4 us.
+// heads over 4, d = 128, window 512, 130 sinks: 11, 48, 85 and 4 us.
 //   warp 0      TMA: K and V
 //   warp 1      issues S and dP (TMEM owner)
 //   warp 2      issues the accumulating products
@@ -479,21 +479,21 @@ __device__ __forceinline__ bool swa_dkv_unit(const SwaBwdParams &p, int u, SwaDk
   return w.t0 < w.t1;
 }
 
-// TMEM of the dK / dV kernel.  D = 64, 80: the halves' S in a ring of three slots of 64
-// columns (P and dS are written back over them), their dP in one slot (a half is read into
-// registers before the next one's products), the accumulators, and K, V and the blocks of
-// ones as the products' left operands: from shared memory a 64-column product takes 48
-// cycles instead of 32, and the loads of the query tiles compete for the same bandwidth
-// (measured at D = 80: 2708 cycles a tile).  D = 128: accumulators of 256 columns leave room
-// for two S and two dP slots only; K and V stay in shared memory.
+// TMEM of the dK / dV kernel: the halves' S in a ring of slots of 64 columns (P and dS are
+// written back over them), their dP in one slot (a half is read into registers before the
+// next one's products), the accumulators, and left operands of the products: from shared
+// memory a 64-column product takes 48 cycles instead of 32, and the loads of the query tiles
+// compete for the same bandwidth.  D = 64, 80: K, V and the blocks of ones (2708 -> 2502
+// cycles a tile at D = 80), and three S slots.  D = 128: the accumulators' 256 columns leave
+// room for K and two slots (two dP slots in its place: 913 against 868 us at 16 heads over 4,
+// 16384 tokens, window 4096).
 template <int D>
 struct SwaTmem {
-  static constexpr bool KV = D != 128;
-  static constexpr int S = KV ? 3 : 2, P = KV ? 1 : 2;
-  static constexpr uint32_t P0 = 64 * S, ACC = 64 * (S + P), K = ACC + 2 * D, V = K + D / 2, ONE = V + D / 2;
-  static_assert((KV ? ONE + 16 : K) <= 512, "TMEM columns");
+  static constexpr bool VT = D != 128;                      // V (and the ones) in TMEM
+  static constexpr int S = VT ? 3 : 2;
+  static constexpr uint32_t P0 = 64 * S, ACC = 64 * (S + 1), K = ACC + 2 * D, V = K + D / 2, ONE = V + D / 2;
+  static_assert((VT ? ONE + 16 : V) <= 512, "TMEM columns");
   static __device__ __forceinline__ uint32_t s_at(uint32_t h) { return 64 * (h % S); }
-  static __device__ __forceinline__ uint32_t p_at(uint32_t h) { return P0 + 64 * (h % P); }
 };
 
 template <int D>
@@ -532,9 +532,9 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const int nunits = swa_dkv_units(p);
 
   using M = typename C::M;
-  if (tid == 0) swa_init_bars(bar, 8, M::KV ? 16 : 1);   // (K, V staged: every elementwise warp)
+  if (tid == 0) swa_init_bars(bar, 8, M::VT ? 16 : 17);   // (every elementwise warp; V's last product)
   // The blocks of ones: columns 0 - 2 (lse) and 3 - 5 (D).
-  for (int r = tid; !M::KV && r < 2 * 128; r += kSwaBwdThreads) {
+  for (int r = tid; !M::VT && r < 2 * 128; r += kSwaBwdThreads) {
     unsigned char *blk = sbase + C::ONE_OFF + (r >> 7) * kSwaExtra;
     const uint4 ones = r < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u);
     *reinterpret_cast<uint4 *>(blk + extra_offset(r & 127, 0)) = ones;
@@ -611,11 +611,9 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       SwaDkvUnit w;
       if (!swa_dkv_unit(p, u, w)) continue;
       const uint32_t ks = kn % C::KS;
-      if (M::KV) ok = mbar_wait_warp(&bar.kv_ready, kn & 1, abort, p.status, site0 + 3);
-      else ok = mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 3);
-      if (!ok) break;
+      if (!(ok = mbar_wait_warp(&bar.kv_ready, kn & 1, abort, p.status, site0 + 3))) break;
       ++kn;
-      const uint32_t kt = base + C::K_OFF + ks * T::TILE, vt = base + C::V_OFF + ks * T::TILE;
+      const uint32_t vt = base + C::V_OFF + ks * T::TILE;
       for (int t = w.t0; ok && t < w.t1; ++t, ++step) {
         const uint32_t st = step % C::QS, ex = base + C::EX_OFF + st * kSwaExtra;
         if (!(ok = mbar_wait_warp(&bar.q_full[st], (step / C::QS) & 1, abort, p.status, site0 + 4))) break;
@@ -626,20 +624,23 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           const uint32_t qt = base + C::Q_OFF + st * T::TILE, gt = base + C::DO_OFF + st * T::TILE;
           tc_fence_after();
           if (elect_one()) {
-            if constexpr (M::KV) swa_scores_tmem<D, 64>(tmem + M::s_at(h), tmem + M::K, qt, 64 * x, tmem + M::ONE, ex);
-            else swa_scores<D, 64>(tmem + M::s_at(h), kt, qt, 64 * x, base + C::ONE_OFF, ex);
+            swa_scores_tmem<D, 64>(tmem + M::s_at(h), tmem + M::K, qt, 64 * x);
+            if constexpr (M::VT) swa_extra_tmem<64>(tmem + M::s_at(h), tmem + M::ONE, 64 * x, ex);
+            else swa_extra<64>(tmem + M::s_at(h), base + C::ONE_OFF, 64 * x, ex);
           }
           __syncwarp();
-          // (One dP slot: read by the half before; two: by the group's own last half.)
-          if (!(ok = M::P == 1 ? mbar_wait_warp(&bar.p_empty[0], (h & 1) ^ 1, abort, p.status, site0 + 10)
-                               : mbar_wait_warp(&bar.p_empty[x], (step & 1) ^ 1, abort, p.status, site0 + 10)))
-            break;
+          if (!(ok = mbar_wait_warp(&bar.p_empty[0], (h & 1) ^ 1, abort, p.status, site0 + 10))) break;
           tc_fence_after();
           if (elect_one()) {
-            if constexpr (M::KV) swa_scores_tmem<D, 64>(tmem + M::p_at(h), tmem + M::V, gt, 64 * x, tmem + M::ONE + 8, ex);
-            else swa_scores<D, 64>(tmem + M::p_at(h), vt, gt, 64 * x, base + C::ONE_OFF + kSwaExtra, ex);
+            if constexpr (M::VT) {
+              swa_scores_tmem<D, 64>(tmem + M::P0, tmem + M::V, gt, 64 * x);
+              swa_extra_tmem<64>(tmem + M::P0, tmem + M::ONE + 8, 64 * x, ex);
+            } else {
+              swa_scores<D, 64>(tmem + M::P0, vt, gt, 64 * x);
+              swa_extra<64>(tmem + M::P0, base + C::ONE_OFF + kSwaExtra, 64 * x, ex);
+            }
             umma_commit(&bar.s_full[x]);
-            if (!M::KV && x == 1 && t == w.t1 - 1) umma_commit(&bar.k_empty[ks]);
+            if (!M::VT && x == 1 && t == w.t1 - 1) umma_commit(&bar.k_empty[ks]);
           }
           __syncwarp();
         }
@@ -697,29 +698,33 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       return v;
     };
     uint32_t kn = 0;
-    // A unit's K (groups 0, 1) and V (2, 3) from shared memory into TMEM, every other 16
-    // values of a row to a group, once the last unit's products have read what was there.
+    // A unit's K (groups 0, 1) and V (2, 3; D = 128: K alone, by all) from shared memory into
+    // TMEM, 16 values of a row in turn to a group, once the last unit's products have read
+    // what was there.
     auto stage_kv = [&]() {
       const uint32_t ks = kn % C::KS;
       if (sc > 0 && !mbar_wait_warp(&bar.s_full[1], (sc - 1) & 1, abort, p.status, site0 + 12)) return false;
       if (!mbar_wait_warp(&bar.k_full[ks], (kn / C::KS) & 1, abort, p.status, site0 + 13)) return false;
       tc_fence_after();
-      const unsigned char *tile = sbase + (x == 0 ? C::K_OFF : C::V_OFF) + ks * T::TILE;
+      const bool isv = M::VT && x == 1;
+      const unsigned char *tile = sbase + (isv ? C::V_OFF : C::K_OFF) + ks * T::TILE;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
-        if ((j & 1) != (grp & 1)) continue;
+        if (M::VT ? (j & 1) != (grp & 1) : (j & 3) != grp) continue;
         uint32_t v[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = 2 * j + e;
           const uint4 a = *reinterpret_cast<const uint4 *>(
-              c < 8 ? tile + r * 128 + ((c ^ (r & 7)) << 4) : tile + T::R0 + r * 32 + (((c - 8) ^ ((r >> 2) & 1)) << 4));
+              c < 8 ? tile + r * 128 + ((c ^ (r & 7)) << 4)
+              : D == 128 ? tile + T::R0 + r * 128 + (((c - 8) ^ (r & 7)) << 4)
+                         : tile + T::R0 + r * 32 + (((c - 8) ^ ((r >> 2) & 1)) << 4));
           v[4 * e] = a.x;
           v[4 * e + 1] = a.y;
           v[4 * e + 2] = a.z;
           v[4 * e + 3] = a.w;
         }
-        tmem_st8(tmem + lane_off + (x == 0 ? M::K : M::V) + 8 * j, v);
+        tmem_st8(tmem + lane_off + (isv ? M::V : M::K) + 8 * j, v);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -732,15 +737,15 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       return true;
     };
     int u = seek(blockIdx.x);
-    if constexpr (M::KV) {
+    if constexpr (M::VT) {
       if (grp == 0) {
         const uint32_t lse1[8] = {0x3F803F80u, 0x00003F80u, 0u, 0u, 0u, 0u, 0u, 0u};
         const uint32_t d1[8] = {0u, 0x3F800000u, 0x3F803F80u, 0u, 0u, 0u, 0u, 0u};
         tmem_st8(tmem + lane_off + M::ONE, lse1);
         tmem_st8(tmem + lane_off + M::ONE + 8, d1);
       }
-      if (u < nunits) ok = stage_kv();
     }
+    if (u < nunits) ok = stage_kv();
     while (ok && u < nunits) {
       const SwaDkvUnit w = nw;
       const int key0 = w.kt * kTileKeys, key = key0 + r;
@@ -754,11 +759,11 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const uint32_t tS = tmem + lane_off + M::s_at(2 * sc + x);
         uint32_t sv[32], pv[32];
         tmem_ld32(tS + sub, sv);
-        tmem_ld32(tmem + lane_off + M::p_at(2 * sc + x) + sub, pv);
+        tmem_ld32(tmem + lane_off + M::P0 + sub, pv);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_empty[M::P == 1 ? 0 : x]);
+        if (lane == 0) mbar_arrive(&bar.p_empty[0]);
         uint32_t pp[16], dd[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -790,9 +795,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       }
       if (!ok) break;
       u = seek(u + gridDim.x);
-      if constexpr (M::KV) {
-        if (u < nunits && !(ok = stage_kv())) break;
-      }
+      if (u < nunits && !(ok = stage_kv())) break;
       if (!(ok = mbar_wait_warp(&bar.acc_full[0], an & 1, abort, p.status, site0 + 9))) break;
       ++an;
       tc_fence_after();

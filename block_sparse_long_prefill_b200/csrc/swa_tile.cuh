@@ -54,10 +54,8 @@ __device__ __forceinline__ void swa_acc32(uint32_t d, uint32_t a, uint32_t tile,
 }
 
 // S (NB columns) = A B^T over the D columns; A and B K-major tiles, B's NB rows from row0 on.
-// extra_a, extra_b: blocks of 16 more columns (32-byte rows, 32-byte swizzle), or 0.
 template <int D, int NB>
-__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int row0, uint32_t extra_a = 0,
-                                           uint32_t extra_b = 0) {
+__device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, int row0) {
   constexpr uint32_t id = idesc_bf16(128, NB, 0, 0);
   const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16) + row0 * 8;
 #pragma unroll
@@ -69,14 +67,12 @@ __device__ __forceinline__ void swa_scores(uint32_t d, uint32_t a, uint32_t b, i
       umma_ss_w(d, al + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128,
                 bl + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128, id, acc);
   }
-  if (extra_a) umma_ss_w(d, desc_lo(extra_a, 16), kHi32, desc_lo(extra_b, 16) + row0 * 2, kHi32, id, 1u);
 }
 
-// The same with A in TMEM (D / 2 columns from a; its 16 more columns from extra_a): the
-// product then takes half of what shared memory has to feed it.
+// The same with A in TMEM (D / 2 columns from a): the product then takes half of what shared
+// memory has to feed it.
 template <int D, int NB>
-__device__ __forceinline__ void swa_scores_tmem(uint32_t d, uint32_t a, uint32_t b, int row0, uint32_t extra_a,
-                                                uint32_t extra_b) {
+__device__ __forceinline__ void swa_scores_tmem(uint32_t d, uint32_t a, uint32_t b, int row0) {
   constexpr uint32_t id = idesc_bf16(128, NB, 0, 0);
   const uint32_t bl = desc_lo(b, 16) + row0 * 8;
 #pragma unroll
@@ -87,7 +83,17 @@ __device__ __forceinline__ void swa_scores_tmem(uint32_t d, uint32_t a, uint32_t
     else
       umma_ts_w(d, a + ks * 8, bl + (ks & 3) * 2 + (ks >> 2) * (SwaTile<D>::R0 / 16), kHi128, id, acc);
   }
-  umma_ts_w(d, extra_a, desc_lo(extra_b, 16) + row0 * 2, kHi32, id, 1u);
+}
+
+// 16 more columns of such a product: blocks of 32-byte rows with the 32-byte swizzle, A's in
+// shared memory or in 8 columns of TMEM.
+template <int NB>
+__device__ __forceinline__ void swa_extra(uint32_t d, uint32_t a, int row0, uint32_t b) {
+  umma_ss_w(d, desc_lo(a, 16), kHi32, desc_lo(b, 16) + row0 * 2, kHi32, idesc_bf16(128, NB, 0, 0), 1u);
+}
+template <int NB>
+__device__ __forceinline__ void swa_extra_tmem(uint32_t d, uint32_t a, int row0, uint32_t b) {
+  umma_ts_w(d, a, desc_lo(b, 16) + row0 * 2, kHi32, idesc_bf16(128, NB, 0, 0), 1u);
 }
 
 template <int D>
