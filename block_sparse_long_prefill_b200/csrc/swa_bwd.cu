@@ -33,8 +33,8 @@
 // are issued before the last item's are summed up.
 // Measured (batch 1, 32 heads, d = 80, N = 16384, window 4096, 4 sinks): statistics 51 us
 // (3.7 TB/s), dQ 855 us (1056 TFLOP/s over its 3 products), dK and dV 1028 us (1171 TFLOP/s
-// over 4), parts 5 us, at a power-capped 1.3-1.6 GHz; a tile takes 1892 and 2270 cycles.  8192 tokens, 8
-// heads over 4, d = 128, window 512, 130 sinks: 11, 48, 85 and 4 us.
+// over 4), parts 5 us, at a power-capped 1.3-1.6 GHz; a tile takes 1892 and 2270 cycles.
+// 8192 tokens, 8 heads over 4, d = 128, window 512, 130 sinks: 11, 48, 85 and 4 us.
 //   warp 0      TMA: K and V
 //   warp 1      issues S and dP (TMEM owner)
 //   warp 2      issues the accumulating products
@@ -484,7 +484,8 @@ __device__ __forceinline__ bool swa_dkv_unit(const SwaBwdParams &p, int u, SwaDk
 // next one's products), the accumulators, and left operands of the products: from shared
 // memory a 64-column product takes 48 cycles instead of 32, and the loads of the query tiles
 // compete for the same bandwidth.  D = 64, 80: K, V and the blocks of ones (2708 -> 2502
-// cycles a tile at D = 80), and three S slots.  D = 128: the accumulators' 256 columns leave
+// cycles a tile at D = 80), and three S slots (two: 147 against 133 us at 32 heads, 4096
+// tokens, window 2048).  D = 128: the accumulators' 256 columns leave
 // room for K and two slots (two dP slots in its place: 913 against 868 us at 16 heads over 4,
 // 16384 tokens, window 4096).
 template <int D>

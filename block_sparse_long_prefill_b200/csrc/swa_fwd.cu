@@ -25,11 +25,13 @@
 // The halves' scores stand in a ring of three slots of 64 columns: a half's next scores wait
 // for the other half's last product, which keeps the halves apart, so that one reads and
 // writes while the other uses the exponential unit (four slots: 112.8 against 106.5 us at
-// D = 64, 8192 tokens, window 2048; 461 against 457 us at D = 128 as above).
+// D = 64, 8192 tokens, window 2048; 461 against 457 us at D = 128).
 //
 // Per 128 x 128 keys 16384 exponentials at 16 a cycle are 1024 cycles; the products are 827
-// cycles at D = 80 and 1291 at D = 128 (64-key products are fed by shared memory: 48 cycles
-// instead of 32).
+// cycles at D = 80 and 1291 at D = 128, where 64-key products are fed by shared memory (48
+// cycles instead of 32).  At D = 128 that is the bound, so Q goes into TMEM as the left operand
+// of S: 1034 cycles (451 -> 432 us as above; at D = 64, where the softmax bounds, the copy
+// costs more than it gives, 106 -> 108 us; at D = 80 TMEM is full).
 // Measured (32 heads, d = 80, N = 16384, window 4096, 4 sinks): 735 us, 820 TFLOP/s at a
 // power-capped 1.4-1.6 GHz, against 811 us with the two streams over query tiles; one
 // 1000-token prompt (4 heads) 10.5 against 16.7 us in a graph, since a walk's chain is half
@@ -99,14 +101,16 @@ struct SwaFwdCfg {
   // then the groups' accumulators.
   static constexpr int S = 3;
   static constexpr uint32_t O = 64 * S;
-  static_assert(O + GRP * D <= 512, "TMEM columns");
+  static constexpr bool QT = D == 128;                         // Q in TMEM as a left operand
+  static constexpr uint32_t Q = O + GRP * D;
+  static_assert(Q + (QT ? D / 2 : 0) <= 512, "TMEM columns");
   static __device__ __forceinline__ uint32_t s_at(uint32_t h) { return 64 * (h % S); }
 };
 
 struct SwaFwdBars {
   uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // per half, of even and odd chunks
-  uint64_t o_full, o_empty, ml_full;
+  uint64_t o_full, o_empty, ml_full, qt_full;
   uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort;
@@ -133,7 +137,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 1);
-      mbar_init(&bar.q_empty[s], 1);
+      mbar_init(&bar.q_empty[s], C::QT ? 2 * C::GRP : 1);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&bar.k_full[s], 1);
@@ -148,6 +152,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         mbar_init(&bar.pv_done[x][s], 1);
       }
     mbar_init(&bar.o_full, 1);
+    mbar_init(&bar.qt_full, 2 * C::GRP);
     mbar_init(&bar.o_empty, 4 * C::GRP);
     mbar_init(&bar.ml_full, 4 * C::GRP);
     mbar_init(&bar.mma_done[0], 1);
@@ -221,7 +226,9 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++qn) {
       const SwaItem w = swa_item(p, u);
       const uint32_t qs = qn % C::QS, qt = base + C::Q_OFF + qs * T::TILE;
-      if (!(ok = mbar_wait_warp(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3))) break;
+      ok = C::QT ? mbar_wait_warp(&bar.qt_full, qn & 1, abort, p.status, site0 + 3)
+                 : mbar_wait_warp(&bar.q_full[qs], (qn / C::QS) & 1, abort, p.status, site0 + 3);
+      if (!ok) break;
       for (int m = 0; ok && m < w.nc; ++m, ++step) {
         const uint32_t ks = step % C::NK, kt = base + C::K_OFF + ks * T::TILE;
         if (!(ok = mbar_wait_warp(&bar.k_full[ks], (step / C::NK) & 1, abort, p.status, site0 + 4))) break;
@@ -234,11 +241,12 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             break;
           tc_fence_after();
           if (elect_one()) {
-            swa_scores<D, 64>(tmem + C::s_at(h), qt, kt, 64 * x);
+            if constexpr (C::QT) swa_scores_tmem<D, 64>(tmem + C::s_at(h), tmem + C::Q, kt, 64 * x);
+            else swa_scores<D, 64>(tmem + C::s_at(h), qt, kt, 64 * x);
             umma_commit(&bar.s_full[x][step & 1]);
             if (x == 1) {
               umma_commit(&bar.k_empty[ks]);
-              if (m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
+              if (!C::QT && m == w.nc - 1) umma_commit(&bar.q_empty[qs]);
             }
           }
           __syncwarp();
@@ -339,6 +347,38 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (lane == 0) mbar_arrive(&bar.o_empty);
       return true;
     };
+    // Q of the CTA's item n from shared memory into TMEM, by the groups of half 1 once the
+    // last item's scores are complete (half 1's of its last chunk are the last).
+    auto stage_q = [&](uint32_t n) {
+      const uint32_t qs = n % C::QS;
+      if (!mbar_wait_warp(&bar.q_full[qs], (n / C::QS) & 1, abort, p.status, site0 + 13)) return false;
+      tc_fence_after();
+      const unsigned char *tile = sbase + C::Q_OFF + qs * T::TILE;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        if (j % (C::GRP / 2) != grp % (C::GRP / 2)) continue;
+        uint32_t v[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = 2 * j + e;
+          const uint4 a = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * T::R0 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+          v[4 * e] = a.x;
+          v[4 * e + 1] = a.y;
+          v[4 * e + 2] = a.z;
+          v[4 * e + 3] = a.w;
+        }
+        tmem_st8(tmem + lane_off + C::Q + 8 * j, v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.q_empty[qs]);
+        mbar_arrive(&bar.qt_full);
+      }
+      return true;
+    };
+    if (C::QT && x == 1 && blockIdx.x < nitems) ok = stage_q(0);
     uint32_t in = 0;                                // items
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++in) {
       const SwaItem w = swa_item(p, u);
@@ -356,6 +396,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if constexpr (C::W == 64) tmem_ld64(tS, sv);
         else tmem_ld32(tS, sv);
         tmem_wait_ld();
+        if (C::QT && x == 1 && m == w.nc - 1 && u + (int)gridDim.x < nitems && !(ok = stage_q(in + 1))) break;
         if (!full) {
 #pragma unroll
           for (int c = 0; c < C::W; c += 32) {
