@@ -35,8 +35,8 @@
 // 64 columns: 1038 against 881 us for dQ), the next scores are issued while these are worked
 // on, and the steps of consecutive items run on without a gap: the next item's first products
 // are issued before the last item's are summed up.
-// Measured (batch 1, 32 heads, d = 80, N = 16384, window 4096, 4 sinks): statistics 51 us
-// (3.7 TB/s), dQ 855 us (1056 TFLOP/s over its 3 products), dK and dV 1028 us (1171 TFLOP/s
+// Measured (batch 1, 32 heads, d = 80, N = 16384, window 4096, 4 sinks): statistics 46 us
+// (4.2 TB/s), dQ 855 us (1056 TFLOP/s over its 3 products), dK and dV 1028 us (1171 TFLOP/s
 // over 4), parts 5 us, at a power-capped 1.3-1.6 GHz; a tile takes 1892 and 2270 cycles.
 // 8192 tokens, 8 heads over 4, d = 128, window 512, 130 sinks: 11, 48, 85 and 4 us.
 //   warp 0      TMA: K and V
@@ -88,8 +88,9 @@ __device__ __forceinline__ void split3(float x, uint32_t *t) {
 
 // ------------------------------------------------------------------ prep
 
+// nb: blocks of a head; their warps take its groups of rows in turn.
 template <int D>
-__global__ void __launch_bounds__(256) swa_bwd_prep_kernel(const SwaBwdParams p) {
+__global__ void __launch_bounds__(256) swa_bwd_prep_kernel(const SwaBwdParams p, int nb) {
   constexpr int LPR = RowLanes<D>::LPR, RPW = RowLanes<D>::RPW;
   const int lane = threadIdx.x & 31;
   const int sub = min(lane / LPR, RPW - 1), v = lane - sub * LPR, base = sub * LPR;
@@ -97,18 +98,17 @@ __global__ void __launch_bounds__(256) swa_bwd_prep_kernel(const SwaBwdParams p)
   const int vv = in ? v : 0;
   const int padded = p.nt * kTileRows;
   const int groups = (padded + RPW - 1) / RPW;
-  const long long tasks = (long long)p.batch * p.hq * groups;
-  const long long nw = (long long)gridDim.x * 8;
-  for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < tasks; task += nw) {
-    const long long bh = task / groups;
-    const int i = (int)(task - bh * groups) * RPW + sub;
-    const int b = (int)(bh / p.hq), h = (int)(bh % p.hq);
+  const long long bh = blockIdx.x / nb;
+  const int b = (int)(bh / p.hq), h = (int)(bh % p.hq);
+  const uint16_t *op = p.out + b * p.o_sb + h * p.o_sh + vv * 8, *gp = p.dout + b * p.do_sb + h * p.do_sh + vv * 8;
+  for (int u = (int)(blockIdx.x % nb) * 8 + (threadIdx.x >> 5); u < groups; u += nb * 8) {
+    const int i = u * RPW + sub;
     const bool live = in && i < p.N;
     float acc = 0.f;
     if (live) {
       float x[8], g[8];
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(p.out + b * p.o_sb + h * p.o_sh + (int64_t)i * p.o_sn + vv * 8)), x);
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(p.dout + b * p.do_sb + h * p.do_sh + (int64_t)i * p.do_sn + vv * 8)), g);
+      unpack8(__ldg(reinterpret_cast<const uint4 *>(op + (int64_t)i * p.o_sn)), x);
+      unpack8(__ldg(reinterpret_cast<const uint4 *>(gp + (int64_t)i * p.do_sn)), g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc = fmaf(x[e], g[e], acc);
     }
@@ -879,10 +879,9 @@ __global__ void __launch_bounds__(256) swa_bwd_join_kernel(const SwaBwdParams p)
 
 template <int D>
 static cudaError_t launch_swa_bwd_d(const CUtensorMap *m, const SwaBwdParams &p, int nsm, cudaStream_t st) {
-  const int groups = (p.nt * kTileRows + RowLanes<D>::RPW - 1) / RowLanes<D>::RPW;
-  long long blocks = ((long long)p.batch * p.hq * groups + 7) / 8;
-  if (blocks > (long long)nsm * 16) blocks = (long long)nsm * 16;
-  swa_bwd_prep_kernel<D><<<(unsigned)blocks, 256, 0, st>>>(p);
+  const int groups = (p.nt * kTileRows + RowLanes<D>::RPW - 1) / RowLanes<D>::RPW, heads = p.batch * p.hq;
+  const int nb = max(1, min((groups + 7) / 8, nsm * 16 / heads));
+  swa_bwd_prep_kernel<D><<<(unsigned)heads * nb, 256, 0, st>>>(p, nb);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
