@@ -511,10 +511,10 @@ struct SwaDkvCfg {
   static constexpr int DO_OFF = Q_OFF + QS * SwaTile<D>::TILE;
   static constexpr int EX_OFF = DO_OFF + QS * SwaTile<D>::TILE;   // a stage's statistics columns
   static constexpr int ONE_OFF = EX_OFF + QS * kSwaExtra;         // ones: lse's columns, D's
-  static constexpr int BAR_OFF = ONE_OFF + 2 * kSwaExtra;
+  using M = SwaTmem<D>;
+  static constexpr int BAR_OFF = ONE_OFF + (M::VT ? 0 : 2 * kSwaExtra);
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
-  using M = SwaTmem<D>;
 };
 
 template <int D>

@@ -97,6 +97,14 @@ def test_backward_of_shared_heads_and_split_sinks(d, batch, hq, hkv, n, window, 
 
 
 @pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("window,sink", [(1, 1), (40, 0), (300, 4), (2000, 150)])
+def test_several_items_a_block(d, window, sink):
+    """More query and key tiles than the GPU has SMs, of walks of one chunk and of many: a
+    block's next item starts while its last one is read out."""
+    _bwd(2, 16, 4, 1100, d, window, sink, seed=window)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
 @pytest.mark.parametrize("up", [True, False])
 def test_scores_that_climb_or_fall_by_hundreds(d, up):
     """Keys whose scores rise along the sequence raise the running maximum in every chunk (by
