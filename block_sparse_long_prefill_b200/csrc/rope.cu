@@ -477,27 +477,29 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kv_append_kernel(const Append
     for (int h = 0; h < nh; ++h) cp_async_16(lane_slot(slots[threadIdx.x >> 5], h), row + h * src.sh);
     cp_async_commit();
   }
-  // The token's sequence and position, and its place in the pages.
-  int seq = t, pos = 0, pid = 0, slot = 0;
+  // The token's sequence and position, and its place in the pages (queries have none there,
+  // but a token without one is left out whole).
+  int seq = t, pos = 0, pid = -1, slot = 0;
   if (p.cu) seq = sequence_of(p.cu, p.batch, lane, RPW, LPR, (int)t0);
   live = live && seq >= 0 && seq < p.batch;
   if (live) {
     const int len = __ldg(p.seq_lens + seq);
     pos = p.cu ? len - __ldg(p.cu + seq + 1) + t : len - 1;
-    bool ok = pos >= 0 && pos < len && (!p.cosp || pos < p.max_pos);
-    if (ok && which != 0) {
+    if (pos >= 0 && pos < len && (!p.cosp || pos < p.max_pos)) {
       const int pg = pos / p.page;
       slot = pos - pg * p.page;
-      ok = pg < p.max_pages;
-      if (ok) {
-        pid = __ldg(p.table + (int64_t)seq * p.max_pages + pg);
-        ok = pid >= 0 && pid < p.num_pages;
-      }
+      if (pg < p.max_pages) pid = __ldg(p.table + (int64_t)seq * p.max_pages + pg);
+    } else {
+      pos = 0;
     }
-    if (!ok) {
-      live = false;
-      record_index_error(p.status, (32 * 16 + 3) * 256);
-    }
+  }
+  // The angles are read while the page id is on its way.
+  const Place pl = place_of(vv, lane, p.cosp ? p.rot : 0, p.interleaved);
+  Vec8 cw, sw;
+  if (which != 2) load_factors(pl, p.cosp, p.sinp, p.rot, pos, wt, vv, lane, cw, sw);
+  if (live && (pid < 0 || pid >= p.num_pages)) {
+    live = false;
+    record_index_error(p.status, (32 * 16 + 3) * 256);
   }
   uint16_t *out;
   int64_t osh;
@@ -517,9 +519,6 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kv_append_kernel(const Append
       if (live) *reinterpret_cast<uint4 *>(out + h * osh) = buf[h * 32 + lane];
     return;
   }
-  const Place pl = place_of(vv, lane, p.cosp ? p.rot : 0, p.interleaved);
-  Vec8 cw, sw;
-  load_factors(pl, p.cosp, p.sinp, p.rot, live ? pos : 0, wt, vv, lane, cw, sw);
   cp_async_wait_all();
 #pragma unroll 2
   for (int h = 0; h < nh; ++h) {

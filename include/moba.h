@@ -352,7 +352,8 @@ int qk_norm_rope_bwd(moba_tensor dq_out, moba_tensor dk_out, moba_tensor q, moba
  *                cosp = sinp = null: no rotation (rot 0)
  * v is copied.  Two tokens with the same place (a page that two sequences extend) leave a row
  * that may hold parts of both.  A token whose position is negative, outside the angle table or
- * on a page that is not there ([0, num_pages)) writes nothing and records MOBA_ERR_INDEX.
+ * on a page that is not there ([0, num_pages)) writes nothing, its query row included, and
+ * records MOBA_ERR_INDEX.
  */
 int kv_append(moba_tensor k, moba_tensor v, moba_tensor q, const int32_t *cu_seqlens,
               const int32_t *seq_lens, const int32_t *page_table, const float *cosp,

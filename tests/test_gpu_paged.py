@@ -328,6 +328,39 @@ def test_append_leaves_out_what_has_no_place():
     assert (c.k[~touched[:, None, :, None].expand(c.k.shape)] == 9).all()
 
 
+@pytest.mark.parametrize("which", ["page", "page id below 0", "behind the table", "angles", "position"])
+def test_append_writes_no_query_of_a_token_without_a_place(which):
+    """The token's key, value and query row are left as they were; its neighbours' are written."""
+    moba = _moba()
+    page, d, hq = 16, 80, 3
+    c = Cache([40, 20, 30], 1, page, d, 14)
+    for x in (c.k, c.v):
+        x.fill_(9)
+    cos, sin = _table(1 << 10, d)
+    table, lens = c.table.clone(), torch.tensor([40, 20, 30], dtype=torch.int32, device="cuda")
+    if which == "page":
+        table[1, 1] = c.k.shape[0]
+    elif which == "page id below 0":
+        table[1, 1] = -1
+    elif which == "behind the table":
+        lens[1] = table.shape[1] * page + 1
+    elif which == "angles":
+        lens[1] = (1 << 10) + 1
+    else:
+        lens[1] = 0
+    x = torch.randn(3, hq + 2, d, generator=torch.Generator("cuda").manual_seed(15), device="cuda").bfloat16()
+    q, k, v = x.split([hq, 1, 1], 1)
+    qo = torch.full((3, hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    moba.kv_append(k, v, c.k, c.v, table, lens, None, cos, sin, q=q, q_out=qo)
+    assert moba.device_status() == -10
+    pos = torch.tensor([39, 29], device="cuda")
+    want, bound = po.norm_rope(q[[0, 2]].double(), None, cos.double()[pos][:, None], sin.double()[pos][:, None], False, EPS)
+    po.check("q", qo[[0, 2]], want, bound)
+    assert (qo[1] == 9).all()
+    written = (c.v != 9).any(1).any(-1).nonzero().tolist()
+    assert sorted(written) == sorted([[int(table[s, p // page]), p % page] for s, p in ((0, 39), (2, 29))])
+
+
 # ------------------------------------------------------------------ in a row
 
 @pytest.mark.parametrize("window,sink", [(0, 0), (50, 4)])
