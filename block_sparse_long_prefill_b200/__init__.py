@@ -566,7 +566,8 @@ def debug_fault_next_launch(kind: int = 1) -> None:
 
 
 def device_status() -> int:
-    """Reads and clears the device-side wait-timeout status (synchronises)."""
+    """Reads and clears the device-side status (synchronises): 0, MOBA_ERR_DEVICE (-7) where a
+    bounded wait ran out, or MOBA_ERR_INDEX (-10) where only an index was out of range."""
     return int(_lib.moba_device_status())
 
 

@@ -13,8 +13,8 @@
 namespace moba {
 
 // Device-side status: status[0] is MOBA_OK, or MOBA_ERR_DEVICE once any bounded wait
-// ran out; status[1] records where the first failing wait was (kernel id * 256 + wait
-// site); status[2] is the wait limit in microseconds (0: the default below);
+// ran out, or MOBA_ERR_INDEX where only an index was out of range; status[1] records where
+// the first of them was (kernel id * 256 + site); status[2] is the wait limit in microseconds (0: the default below);
 // status[3] is a one-shot test flag (see moba_debug_fault_next_launch).  The words live
 // in the library's module (api.cu); kernels get their address as a parameter, and
 // moba_device_status() reads and clears the first two.
@@ -38,14 +38,15 @@ __device__ __forceinline__ unsigned long long global_timer_ns() {
   return t;
 }
 
+// A wait that ran out left a launch unfinished: it takes the place of an index error.
 __device__ __forceinline__ void record_device_error(int *status, int site) {
-  if (atomicCAS(&status[0], MOBA_OK, MOBA_ERR_DEVICE) == MOBA_OK) atomicExch(&status[1], site);
+  if (atomicExch(&status[0], MOBA_ERR_DEVICE) != MOBA_ERR_DEVICE) atomicExch(&status[1], site);
 }
 
 // An index in device memory (a position, a page id, a length) is out of range: the access
 // it names is left out.
 __device__ __forceinline__ void record_index_error(int *status, int site) {
-  if (atomicCAS(&status[0], MOBA_OK, MOBA_ERR_INDEX) == MOBA_OK) atomicExch(&status[1], site);
+  if (atomicCAS(&status[0], MOBA_OK, MOBA_ERR_INDEX) == MOBA_OK) atomicCAS(&status[1], 0, site);
 }
 
 // ------------------------------------------------------------------ mbarrier

@@ -385,8 +385,9 @@ int paged_decode_attn(moba_tensor q, moba_tensor k_pages, moba_tensor v_pages,
 
 /*
  * Reads and clears the device-side status word that bounded kernel waits and index checks
- * write (MOBA_OK, MOBA_ERR_DEVICE or MOBA_ERR_INDEX) on the current device.  Synchronises
- * the device.
+ * write (MOBA_OK, MOBA_ERR_DEVICE or MOBA_ERR_INDEX) on the current device.  Where both
+ * happened since the last read it is MOBA_ERR_DEVICE: that launch is unfinished.
+ * Synchronises the device.
  */
 int moba_device_status(void);
 

@@ -41,3 +41,35 @@ def test_a_wait_that_runs_out_reports_an_error_and_the_context_stays_usable():
     rows = np.arange(w.seqlen, dtype=np.int32)
     out_o, lse_o = oracle.swa(q, k, v, window=w.window, rows=rows)
     check_out(out2.float().cpu().numpy(), lse2.cpu().numpy(), out_o, lse_o)
+
+
+def _bad_index(moba):
+    """A rotation whose one row has no angles: MOBA_ERR_INDEX."""
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros(1, 8, device="cuda")
+    moba.qk_norm_rope_fwd(x, x, t, t, torch.full((1, 1), -1, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("index_first", [True, False])
+def test_a_wait_that_runs_out_is_not_hidden_by_a_bad_index(index_first):
+    """Both errors between two reads of the status, in either order: the one that left a
+    launch unfinished is reported."""
+    import block_sparse_long_prefill_b200 as moba
+    w = workloads.small_swa(batch=1, hq=2, hkv=2, seqlen=1024, d=64, window=256)
+    q, k, v = (t.cuda() for t in workloads.make_inputs(w, 18))
+    assert moba.device_status() == 0
+    try:
+        moba.debug_set_wait_limit_us(2000)
+        if index_first:
+            _bad_index(moba)
+        moba.debug_fault_next_launch(1)
+        moba.swa_attn_fwd(q, k, v, w.window)
+        if not index_first:
+            _bad_index(moba)
+        assert moba.device_status() == MOBA_ERR_DEVICE
+    finally:
+        moba.debug_fault_next_launch(0)
+        moba.debug_set_wait_limit_us(0)
+    assert moba.device_status() == 0
+    _bad_index(moba)
+    assert moba.device_status() == -10 and moba.device_status() == 0
