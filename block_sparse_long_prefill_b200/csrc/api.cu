@@ -594,6 +594,7 @@ int swa_sink_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, in
   if ((rc = check_tensor(q)) || (rc = check_tensor(k)) || (rc = check_tensor(v)) ||
       (rc = check_tensor(out)))
     return rc;
+  if (!writable(out, batch, hq, N)) return MOBA_ERR_ARG;
   if (!lse) return MOBA_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOBA_ERR_ALIGN;
   int nsm = 0;

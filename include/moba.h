@@ -255,8 +255,10 @@ int moba_attn_bwd(moba_tensor q, moba_tensor k, moba_tensor v, moba_tensor out, 
  * granularity; moba_select_static has them at block granularity): swa_attn_fwd_chunk with
  * M_ij = 0 iff j <= p_i and (p_i - j < window or j < sink), p_i = Nk - N + i.
  *   sink : >= 0 (MOBA_ERR_ARG otherwise); 0 is swa_attn_fwd_chunk
- * The other arguments and errors are swa_attn_fwd_chunk's.  k and v must be finite also at
- * positions that a row does not see (they are multiplied by zero).
+ * The other arguments and errors are swa_attn_fwd_chunk's.  In all three sliding-window calls,
+ * and in every call below, an output whose elements share an address through a zero stride is
+ * MOBA_ERR_ARG.  k and v must be finite also at positions that a row does not see (they are
+ * multiplied by zero).
  */
 int swa_sink_attn_fwd(moba_tensor q, moba_tensor k, moba_tensor v, int batch, int hq, int hkv,
                       int N, int Nk, int d, int window, int sink, float scale, moba_tensor out,

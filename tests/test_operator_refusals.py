@@ -47,6 +47,18 @@ def test_sink_forward(kw, code):
     assert _fwd(**kw) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(out=ZERO), ARG), (dict(out=T(1 << 20, 8 * 1024, 0, 128)), ARG), (dict(out=T(1 << 20, 0, 8 * 1024, 128), batch=2), ARG),
+    (dict(out=ZERO, sink=0), ARG)])
+def test_sink_forward_into_an_output_whose_rows_share_an_address(kw, code):
+    assert _fwd(**kw) == code
+
+
+@NO_GPU
+def test_a_stride_of_zero_over_one_element_is_fine():
+    assert _fwd(out=T(1 << 20, 0, 8 * 1024, 128)) == _fwd(out=ZERO, N=1) == NODEVICE
+
+
 def _bwd(q=OK, dq=OK, dk=OK, lse=P, ws=P, nbytes=1 << 40, batch=1, hq=2, hkv=1, N=300, d=128, window=10, sink=4):
     return moba.library().swa_attn_bwd(q, OK, OK, OK, OK, lse, batch, hq, hkv, N, d, window, sink, 0.0, dq, dk, OK, ws,
                                        nbytes, None)
