@@ -916,8 +916,9 @@ int paged_decode_attn(moba_tensor q, moba_tensor k_pages, moba_tensor v_pages,
   if (!lse) return MOBA_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOBA_ERR_ALIGN;
   const int G = hq / hkv, ngrp = (G + kDecodeRows - 1) / kDecodeRows;
-  // Tiles are counted in 32 bits, sequences x items in one grid dimension.
-  const double tiles = (double)batch * hkv * ngrp * ((double)max_pages * page / 16 + 16);
+  // Tiles (and a run's rounding, up to a grid's more) are counted in 32 bits, sequences x items
+  // in one grid dimension.
+  const double tiles = (double)batch * hkv * ngrp * ((double)max_pages * page / 16 + 16) + kDecodeCtas;
   if (tiles >= 2147483648.0 || (double)max_pages * page >= 2147483648.0) return MOBA_ERR_SHAPE;
   size_t off_o = 0, off_l = 0;
   const size_t need = decode_workspace_bytes(batch, d, &off_o, &off_l);

@@ -146,6 +146,14 @@ def test_decode(kw, code):
     assert _decode(**kw) == code
 
 
+def test_decode_counts_its_work_and_the_run_of_the_last_block_in_32_bits():
+    """The work is dealt out in runs of ceil(work / blocks): the sum of both has to fit too.
+    8 sequences of 2 KV heads; an item of w pages of 16 costs up to w + 8 tiles."""
+    w = (1 << 27) - 17
+    assert 16 * (w + 8) + 443 >= 1 << 31            # (work + blocks - 1)
+    assert _decode(batch=8, page=16, width=w) == SHAPE
+
+
 @NO_GPU
 def test_valid_calls_without_a_device_report_no_device():
     assert _fwd() == _bwd() == _rope() == _rope(True) == _append() == _decode() == NODEVICE
