@@ -188,6 +188,20 @@ def _stream(stream) -> ctypes.c_void_p:
 _NO_STREAM = contextlib.nullcontext()
 
 
+def _own_stream(fn: str, stream, q):
+    """``stream`` as a torch stream on the device of the call's first tensor.  As in the prefill
+    calls any object with a ``cuda_stream`` handle will do; one that names another device than
+    the tensors' is refused."""
+    if stream is None or not getattr(q, "is_cuda", False):   # (the binding names what q is)
+        return None
+    dev = getattr(stream, "device", None)
+    if isinstance(dev, torch.device) and dev.index is not None and dev != q.device:
+        raise ValueError(f"{fn}: the stream is on {dev}, the tensors are on {q.device}")
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=q.device)
+
+
 def _on_stream(stream):
     """Makes ``stream`` (None: as it is) the current stream of its device, so that what a
     call allocates belongs to the stream that uses it."""
@@ -309,6 +323,7 @@ def swa_attn_fwd_chunk(q, k, v, window: int, scale: float = 0.0, out=None, lse=N
                        sink: int = 0):
     """Sliding-window attention of the last N positions (q) over k.shape[2] positions, the
     first ``sink`` of them staying visible behind the window."""
+    stream = _own_stream("swa_attn_fwd", stream, q)
     with _on_stream(stream):
         rc, out, lse = _binding.swa_fwd(q, k, v, window, sink, scale, out, lse)
     _check("swa_attn_fwd", rc)
@@ -328,6 +343,7 @@ def swa_attn_bwd(q, k, v, out, lse, dout, window: int, sink: int = 0, scale: flo
                  dk=None, dv=None, workspace=None, stream=None):
     """Gradients of swa_attn_fwd (``window``, ``sink`` and ``scale`` as given to it) for whole
     sequences.  Returns (dq, dk, dv), bf16."""
+    stream = _own_stream("swa_attn_bwd", stream, q)
     with _on_stream(stream):
         rc, dq, dk, dv = _binding.swa_bwd(q, k, v, out, lse, dout, window, sink, scale, dq, dk, dv, workspace)
     _check("swa_attn_bwd", rc)
@@ -342,6 +358,7 @@ def qk_norm_rope_fwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=Non
     float32 [positions, rot / 2]; the first rot columns turn, in pairs (i, i + rot / 2) or,
     interleaved, of neighbours.  positions: int32 [b, N] (default: row n is at n).  Returns
     (q_out [b, hq, N, d], k_out [b, hkv, N, d]) bf16, which may be given as q and k."""
+    stream = _own_stream("qk_norm_rope_fwd", stream, q)
     with _on_stream(stream):
         rc, q_out, k_out = _binding.rope_fwd(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved,
                                              q_out, k_out)
@@ -356,6 +373,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=No
     """Gradients of qk_norm_rope_fwd for the gradients dq_out, dk_out of its results and its
     inputs q, k.  Returns (dq, dk, dq_weight, dk_weight): bf16, and float32 [d] or None where
     there is no weight."""
+    stream = _own_stream("qk_norm_rope_bwd", stream, dq_out)
     with _on_stream(stream):
         rc, dq, dk, dq_weight, dk_weight = _binding.rope_bwd(dq_out, dk_out, q, k, cos, sin, positions, q_weight,
                                                              k_weight, eps, interleaved, dq, dk, workspace)
@@ -375,6 +393,7 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos
     b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (default: one token a sequence).
     With q [T, hq, d], returns the queries normalised and rotated to the same positions
     (tokens behind the last sequence are left as they were), else None."""
+    stream = _own_stream("kv_append", stream, k)
     with _on_stream(stream):
         rc, q_out = _binding.append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, cos, sin, k_weight,
                                     eps, interleaved, q, q_weight, q_out)
@@ -397,6 +416,7 @@ def paged_decode_attn(q, k_pages, v_pages, page_table, seq_lens, window: int = 0
     kv_append ([MoBA] §실험: block-sparse prefill, full attention while decoding; with a
     window, what swa_attn_fwd computes for the last position).  The query of sequence b sits
     at position seq_lens[b] - 1.  Returns (out bf16 [batch, hq, d], lse float32 [batch, hq])."""
+    stream = _own_stream("paged_decode_attn", stream, q)
     with _on_stream(stream):
         rc, out, lse = _binding.decode(q, k_pages, v_pages, page_table, seq_lens, window, sink, scale, out, lse,
                                        workspace)

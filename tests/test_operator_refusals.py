@@ -186,3 +186,31 @@ def test_the_binding_takes_cuda_tensors_only():
         moba.swa_attn_fwd(x[0], x, x, 3)
     with pytest.raises(ValueError, match="dimensions"):
         moba.paged_decode_attn(x, x, x, i, i[:, 0])
+
+
+class _Handle:
+    """A stream of some other library: its handle alone."""
+    cuda_stream = 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    """(Tensors and streams of two GPUs, described.)"""
+    class Tensor:
+        is_cuda, device = True, torch.device("cuda", 0)
+
+    class Elsewhere(_Handle):
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="the stream is on cuda:1, the tensors are on cuda:0"):
+        moba._own_stream("paged_decode_attn", Elsewhere(), Tensor())
+    assert moba._own_stream("paged_decode_attn", None, Tensor()) is None
+
+
+def test_with_a_stream_the_tensors_are_still_named():
+    t = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    x = torch.zeros(1, 2, 5, 64, dtype=torch.bfloat16)
+    i = torch.zeros(5, 1, dtype=torch.int32)
+    for call in (lambda: moba.paged_decode_attn(t, x, x, i, i[:, 0], stream=_Handle()),
+                 lambda: moba.swa_attn_fwd(x, x, x, 3, stream=_Handle())):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
