@@ -8,6 +8,12 @@ functions here only turn torch tensors into pointers, strides and a stream and p
 them through the C ABI: every step of the computation runs in the library's sm_100a
 kernels.  There is no CPU fallback; importing fails loudly when either is missing.
 
+Every call runs on the current stream of its tensors' device, or on ``stream``: then the
+caller orders it behind what made the inputs and before what reads the results
+(``wait_stream``), as with any torch stream.  The calls around the attention (and
+swa_attn_fwd) keep the memory of inputs and results until both streams are done with it, so
+either may be dropped at any time.
+
 Method sources (by page title and section):
   [MoBA] "MoBA: 어텐션에 전문가 혼합을 적용해 긴 문맥을 효율적으로 처리하는 블록 어텐션
          (feat. MoonshotAI)", PyTorch KR forum summary of the MoBA paper.
@@ -208,10 +214,15 @@ def _on_stream(stream):
     return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
-def _hand_over(stream, *results):
-    """Results allocated on ``stream`` go to a caller on the current stream, which may drop
-    them with work of its own still to come."""
+def _hand_over(stream, inputs, results):
+    """What a call on ``stream`` takes and gives belongs to two streams: the inputs (and results
+    that were given) may be dropped by a caller on its own stream before the kernels are done
+    with them, and results allocated on ``stream`` with work of the caller's still to come.
+    Their memory is not handed out again before both streams have finished.  (None: one stream.)"""
     if stream is not None:
+        for t in (*inputs, *results):
+            if t is not None:
+                t.record_stream(stream)
         for t in results:
             if t is not None:
                 t.record_stream(torch.cuda.current_stream(t.device))
@@ -327,7 +338,7 @@ def swa_attn_fwd_chunk(q, k, v, window: int, scale: float = 0.0, out=None, lse=N
     with _on_stream(stream):
         rc, out, lse = _binding.swa_fwd(q, k, v, window, sink, scale, out, lse)
     _check("swa_attn_fwd", rc)
-    _hand_over(stream, out, lse)
+    _hand_over(stream, (q, k, v), (out, lse))
     return out, lse
 
 
@@ -347,7 +358,7 @@ def swa_attn_bwd(q, k, v, out, lse, dout, window: int, sink: int = 0, scale: flo
     with _on_stream(stream):
         rc, dq, dk, dv = _binding.swa_bwd(q, k, v, out, lse, dout, window, sink, scale, dq, dk, dv, workspace)
     _check("swa_attn_bwd", rc)
-    _hand_over(stream, dq, dk, dv)
+    _hand_over(stream, (q, k, v, out, lse, dout, workspace), (dq, dk, dv))
     return dq, dk, dv
 
 
@@ -363,7 +374,7 @@ def qk_norm_rope_fwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=Non
         rc, q_out, k_out = _binding.rope_fwd(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved,
                                              q_out, k_out)
     _check("qk_norm_rope_fwd", rc)
-    _hand_over(stream, q_out, k_out)
+    _hand_over(stream, (q, k, cos, sin, positions, q_weight, k_weight), (q_out, k_out))
     return q_out, k_out
 
 
@@ -378,7 +389,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=No
         rc, dq, dk, dq_weight, dk_weight = _binding.rope_bwd(dq_out, dk_out, q, k, cos, sin, positions, q_weight,
                                                              k_weight, eps, interleaved, dq, dk, workspace)
     _check("qk_norm_rope_bwd", rc)
-    _hand_over(stream, dq, dk, dq_weight, dk_weight)
+    _hand_over(stream, (dq_out, dk_out, q, k, cos, sin, positions, q_weight, k_weight, workspace),
+               (dq, dk, dq_weight, dk_weight))
     return dq, dk, dq_weight, dk_weight
 
 
@@ -398,7 +410,8 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos
         rc, q_out = _binding.append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, cos, sin, k_weight,
                                     eps, interleaved, q, q_weight, q_out)
     _check("kv_append", rc)
-    _hand_over(stream, q_out)
+    _hand_over(stream, (k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, cos, sin, k_weight, q,
+                        q_weight), (q_out,))
     return q_out
 
 
@@ -421,7 +434,7 @@ def paged_decode_attn(q, k_pages, v_pages, page_table, seq_lens, window: int = 0
         rc, out, lse = _binding.decode(q, k_pages, v_pages, page_table, seq_lens, window, sink, scale, out, lse,
                                        workspace)
     _check("paged_decode_attn", rc)
-    _hand_over(stream, out, lse)
+    _hand_over(stream, (q, k_pages, v_pages, page_table, seq_lens, workspace), (out, lse))
     return out, lse
 
 

@@ -1,5 +1,5 @@
 """The calls around the prefill on a stream of the caller's choice: any object with a stream
-handle, as the prefill takes it."""
+handle, as the prefill takes it, and inputs that are dropped while the call still waits."""
 import pytest
 import torch
 
@@ -91,3 +91,40 @@ def test_any_object_with_a_stream_handle(name):
     side.synchronize()
     assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(want, got))
     assert _moba().device_status() == 0
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_inputs_stay_until_they_are_read(name):
+    """The call's stream is busy; its inputs are dropped and the caller goes on allocating: the
+    memory must not be handed out again before the call has read it."""
+    x, call = CALLS[name]()
+    want = call(x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    copies = {n: t.clone() for n, t in x.items()}
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    got = call(copies, stream=side)
+    copies.clear()
+    junk = [torch.full_like(t, 1) for t in x.values() for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(want, got))
+    assert _moba().device_status() == 0 and junk
+
+
+def test_given_results_stay_until_they_are_written():
+    """An output of the caller's that is dropped before the call writes it: what is allocated
+    meanwhile must not be written over."""
+    moba = _moba()
+    x = _swa_fwd()[0]
+    side = torch.cuda.Stream()
+    out = torch.empty_like(x["q"])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    moba.swa_attn_fwd(x["q"], x["k"], x["v"], 100, sink=5, out=out, stream=side)
+    del out
+    junk = [torch.full_like(x["q"], 9) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all((t == 9).all() for t in junk)
