@@ -6,7 +6,8 @@ A thin binding over ``libmoba.so`` (declared in ``include/moba.h``): ctypes, and
 module (``_binding``) for the calls that take about as long on the host as on the GPU.  The
 functions here only turn torch tensors into pointers, strides and a stream and pass
 them through the C ABI: every step of the computation runs in the library's sm_100a
-kernels.  There is no CPU fallback; importing fails loudly when either is missing.
+kernels.  There is no CPU fallback: importing fails when the library is missing, and the
+calls that need the compiled module when that is.
 
 Every call runs on the current stream of its tensors' device, or on ``stream``: then the
 caller orders it behind what made the inputs and before what reads the results
@@ -24,9 +25,12 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.util
 import os
 
 import torch
+
+from .build import binding_path
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoba.so")
@@ -69,7 +73,7 @@ class MobaWeight(ctypes.Structure):
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
-                          "`python -m block_sparse_long_prefill_b200.build` (nvcc, sm_100a)")
+                          "`python block_sparse_long_prefill_b200/build.py` (nvcc, sm_100a)")
     lib = ctypes.CDLL(LIB_PATH)
     I, P, S = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
     T = MobaTensor
@@ -116,20 +120,23 @@ def _load():
 _lib = _load()
 
 
-def _load_binding():
-    """The compiled binding of the short calls (csrc/binding.cpp), beside the library."""
-    import importlib.util
-    path = os.path.join(_HERE, "_binding.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with "
-                          "`python -m block_sparse_long_prefill_b200.build` (nvcc, g++)")
-    spec = importlib.util.spec_from_file_location("_binding", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    return mod
+class _Binding:
+    """The compiled binding of the short calls (csrc/binding.cpp), loaded when one is first
+    called: it fits one torch and one Python, and the prefill needs the library alone."""
+
+    def __getattr__(self, name):
+        path = binding_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with "
+                              "`python block_sparse_long_prefill_b200/build.py` (nvcc, g++)")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        self.__dict__.update((n, f) for n, f in vars(mod).items() if not n.startswith("_"))
+        return getattr(mod, name)
 
 
-_binding = _load_binding()
+_binding = _Binding()
 
 
 def library() -> ctypes.CDLL:
@@ -330,13 +337,34 @@ def moba_attn_fwd_chunk(q, k, v, idx, block: int, topk: int, workspace: torch.Te
     return out, lse
 
 
+def _swa_fwd(q, k, v, window, sink, scale, out, lse):
+    """The compiled binding's swa_fwd without it, like the other prefill calls."""
+    b, hq, N, d = q.shape
+    hkv, Nk = k.shape[1], k.shape[2]
+    dev = _device("swa_attn_fwd", ("q", q, _BF16, False, None), ("k", k, _BF16, False, (b, hkv, Nk, d)),
+                  ("v", v, _BF16, False, (b, hkv, Nk, d)), ("out", out, _BF16, False, (b, hq, N, d)),
+                  ("lse", lse, _F32, True, (b, hq, N)))
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(b, hq, N, dtype=torch.float32, device=dev)
+        rc = _lib.swa_sink_attn_fwd(_t(q), _t(k), _t(v), b, hq, hkv, N, Nk, d, window, sink, float(scale),
+                                    _t(out), lse.data_ptr(), _stream(None))
+    return rc, out, lse
+
+
 def swa_attn_fwd_chunk(q, k, v, window: int, scale: float = 0.0, out=None, lse=None, stream=None,
                        sink: int = 0):
     """Sliding-window attention of the last N positions (q) over k.shape[2] positions, the
     first ``sink`` of them staying visible behind the window."""
     stream = _own_stream("swa_attn_fwd", stream, q)
     with _on_stream(stream):
-        rc, out, lse = _binding.swa_fwd(q, k, v, window, sink, scale, out, lse)
+        try:
+            call = _binding.swa_fwd
+        except ImportError:
+            call = _swa_fwd
+        rc, out, lse = call(q, k, v, window, sink, scale, out, lse)
     _check("swa_attn_fwd", rc)
     _hand_over(stream, (q, k, v), (out, lse))
     return out, lse

@@ -10,7 +10,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoba.so")
-BINDING = os.path.join(PKG, "_binding.so")   # the compiled binding of the short calls (binding.cpp)
 SOURCES = ["api.cu", "select.cu", "gate.cu", "attn.cu", "merge.cu", "noalloc.cu", "bwd.cu",
            "swa_fwd.cu", "swa_bwd.cu", "rope.cu", "decode.cu"]
 HEADERS = ["common.cuh", "params.h", "lists.cuh", "rows.cuh", "swa_tile.cuh"]
@@ -21,6 +20,15 @@ NVCC_FLAGS = [
     "--expt-relaxed-constexpr",
     "-Xcompiler", "-fPIC", "-shared",
 ]
+
+
+def binding_path() -> str:
+    """The compiled binding of the short calls (binding.cpp).  It is built against one torch and
+    one Python; its name says which, so that another finds none instead of a wrong one."""
+    import importlib.machinery
+
+    import torch
+    return os.path.join(PKG, f"_binding-{torch.__version__}{importlib.machinery.EXTENSION_SUFFIXES[0]}")
 
 
 def _nvcc() -> str:
@@ -39,13 +47,14 @@ def _stale() -> bool:
 
 
 def _build_binding(verbose: bool = False) -> None:
-    """Compile _binding.so against the installed torch; it finds libmoba.so beside itself."""
+    """Compile the binding against the installed torch; it finds libmoba.so beside itself."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING + f".tmp{os.getpid()}"
+    path = binding_path()
+    tmp = path + f".tmp{os.getpid()}"
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -56,7 +65,7 @@ def _build_binding(verbose: bool = False) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, BINDING)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -64,7 +73,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     source is compiled to an object file in parallel, then the objects are linked."""
     if force or _stale():
         _build_library(verbose, extra)
-    if force or _older(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "moba.h")]):
+    if force or _older(binding_path(), [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "moba.h")]):
         _build_binding(verbose)
     return LIB
 

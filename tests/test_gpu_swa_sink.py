@@ -235,3 +235,27 @@ def test_results_of_another_stream_stay_until_they_are_read():
         junk = [torch.full_like(q, 9.0) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(junk) == 4
+
+
+def test_forward_without_the_compiled_binding(monkeypatch):
+    """Another torch finds no binding; the forward then goes through ctypes, like the prefill."""
+    moba = _moba()
+    q, k, v, _ = _inputs(2, 4, 2, 300, 500, 80, 9)
+    want = [moba.swa_attn_fwd_chunk(q, k, v, 77, 0.2, sink=s) for s in (0, 5)]
+
+    class Missing:
+        def __getattr__(self, name):
+            raise ImportError(name)
+
+    monkeypatch.setattr(moba, "_binding", Missing())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for s, (out, lse) in zip((0, 5), want):
+        for stream in (None, side):
+            o, l = moba.swa_attn_fwd_chunk(q, k, v, 77, 0.2, stream=stream, sink=s)
+            torch.cuda.synchronize()
+            assert torch.equal(o, out) and torch.equal(l, lse)
+    with pytest.raises(ValueError, match="k has shape"):
+        moba.swa_attn_fwd(q, k[:1], v, 77)
+    with pytest.raises(ImportError):
+        moba.swa_attn_bwd(q, q, q, q, lse, q, 77)
