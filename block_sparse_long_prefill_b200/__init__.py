@@ -621,8 +621,9 @@ def debug_set_wait_limit_us(microseconds: int) -> None:
 
 
 def debug_fault_next_launch(kind: int = 1) -> None:
-    """Test hook: the next attention launch leaves one load undone so that a bounded wait
-    runs out (MOBA_ERR_DEVICE from device_status()); 0 clears a pending request."""
+    """Test hook: the next attention launch (2: dK / dV launch of swa_attn_bwd) leaves one load
+    or announcement undone so that a bounded wait runs out (MOBA_ERR_DEVICE from
+    device_status()); 0 clears a pending request."""
     _check("moba_debug_fault_next_launch", _lib.moba_debug_fault_next_launch(int(kind)))
 
 

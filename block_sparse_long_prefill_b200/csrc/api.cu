@@ -965,7 +965,7 @@ int moba_debug_set_wait_limit_us(int microseconds) {
 }
 
 int moba_debug_fault_next_launch(int kind) {
-  if (kind < 0 || kind > 1) return MOBA_ERR_ARG;
+  if (kind < 0 || kind > 2) return MOBA_ERR_ARG;
   if (cudaDeviceSynchronize() != cudaSuccess) return MOBA_ERR_LAUNCH;
   if (cudaMemcpyToSymbol(g_device_status, &kind, sizeof(int), 3 * sizeof(int)) != cudaSuccess)
     return MOBA_ERR_LAUNCH;

@@ -254,33 +254,30 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
   if (warp == 0) {
     // ------------------------------------------------------------ V and K
-    uint32_t cnt = 0;
+    uint32_t nv = 0, nk = 0;                        // issued
     bool ok = true;
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
       const SwaDqItem w = swa_dq_item(p, u);
-      for (int m = 0; m < w.nc; ++m, ++cnt) {
-        const uint32_t vs = cnt % C::NV, ks = cnt % C::NK;
-        if (!(ok = mbar_wait_warp(&bar.v_empty[vs], ((cnt / C::NV) & 1) ^ 1, abort, p.status, site0 + 1))) break;
+      for (int m = 0; m < w.nc; ++m) {
+        const uint32_t vs = nv % C::NV, ks = nk % C::NK;
+        if (!(ok = mbar_wait_warp(&bar.v_empty[vs], ((nv / C::NV) & 1) ^ 1, abort, p.status, site0 + 1))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bar.v_full[vs], T::BYTES);
           swa_load_tile<D>(sbase + C::V_OFF + vs * T::TILE, &tmV, &tmV1, &bar.v_full[vs], swa_dq_key(w, m), w.hk, w.b);
         }
         __syncwarp();
-        if (!(ok = mbar_wait_warp(&bar.k_empty[ks], ((cnt / C::NK) & 1) ^ 1, abort, p.status, site0 + 1))) {
-          ++cnt;       // (V was issued)
-          break;
-        }
+        ++nv;
+        if (!(ok = mbar_wait_warp(&bar.k_empty[ks], ((nk / C::NK) & 1) ^ 1, abort, p.status, site0 + 1))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bar.k_full[ks], T::BYTES);
           swa_load_tile<D>(sbase + C::K_OFF + ks * T::TILE, &tmK, &tmK1, &bar.k_full[ks], swa_dq_key(w, m), w.hk, w.b);
         }
         __syncwarp();
+        ++nk;
       }
     }
-    if (*abort) {
-      drain_ring(bar.v_full, cnt, C::NV, p.status);
-      drain_ring(bar.k_full, cnt, C::NK, p.status);
-    }
+    drain_ring(bar.v_full, nv, C::NV, p.status);
+    drain_ring(bar.k_full, nk, C::NK, p.status);
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q and dO
     uint32_t cnt = 0;
@@ -295,7 +292,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       __syncwarp();
     }
-    if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
+    drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S and dP
     // Of each chunk, as soon as the last chunk's have been read into registers.
@@ -324,6 +321,7 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     swa_issued(&bar.mma_done[0], p.status);
   } else if (warp == 2) {
     // ------------------------------------------------------------ dQ += dS K
+    const bool mute = swa_take_fault(p.status, 1);
     uint32_t step = 0, an = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++an) {
@@ -337,9 +335,11 @@ swa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           const uint32_t kt = base + C::K_OFF + ks * T::TILE, tS = tmem + C::DS0 + 64 * (step & 1);
           swa_acc<D>(tmem + C::ACC, tS, kt, 0, m == 0);
           swa_acc<D>(tmem + C::ACC, tS + 32, kt, 1, false);
-          umma_commit(&bar.slot_empty[step & 1]);
-          umma_commit(&bar.k_empty[ks]);
-          if (m == w.nc - 1) umma_commit(&bar.acc_full[0]);
+          if (!mute || step > 0) {
+            umma_commit(&bar.slot_empty[step & 1]);
+            umma_commit(&bar.k_empty[ks]);
+            if (m == w.nc - 1) umma_commit(&bar.acc_full[0]);
+          }
         }
         __syncwarp();
       }
@@ -578,7 +578,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       __syncwarp();
       ++cnt;
     }
-    if (*abort) drain_ring(bar.k_full, cnt, C::KS, p.status);
+    drain_ring(bar.k_full, cnt, C::KS, p.status);
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q, dO, row statistics
     uint32_t cnt = 0;
@@ -605,7 +605,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         }
       }
     }
-    if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
+    drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S^T and dP^T
     // Per query tile and half x: S^T as soon as the S slot's write-back has been consumed,
@@ -654,6 +654,7 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     swa_issued(&bar.mma_done[0], p.status);
   } else if (warp == 2) {
     // ------------------------------------------------------------ dV += P^T dO, dK += dS^T Q
+    const bool mute = swa_take_fault(p.status, 2);
     const uint32_t tK = tmem + M::ACC, tV = tK + D;
     uint32_t step = 0, an = 0;
     bool ok = true;
@@ -676,10 +677,12 @@ swa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const uint32_t tS = tmem + M::s_at(h);   // of 32 queries: P^T, then dS^T
             swa_acc<D, 16>(tV, tS, gp, x, x == 0 && t == w.t0);
             swa_acc<D, 16>(tK, tS + 16, qp, x, x == 0 && t == w.t0);
-            umma_commit(&bar.slot_empty[h % M::S]);
-            if (x == 1) {
-              umma_commit(&bar.q_empty[st]);
-              if (t == w.t1 - 1) umma_commit(&bar.acc_full[0]);
+            if (!mute || step > 0) {
+              umma_commit(&bar.slot_empty[h % M::S]);
+              if (x == 1) {
+                umma_commit(&bar.q_empty[st]);
+                if (t == w.t1 - 1) umma_commit(&bar.acc_full[0]);
+              }
             }
           }
           __syncwarp();

@@ -177,33 +177,30 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
   if (warp == 0) {
     // ------------------------------------------------------------ K and V
-    uint32_t cnt = 0;
+    uint32_t nk = 0, nv = 0;                        // issued
     bool ok = true;
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x) {
       const SwaItem w = swa_item(p, u);
-      for (int m = 0; m < w.nc; ++m, ++cnt) {
-        const uint32_t ks = cnt % C::NK, vs = cnt % C::NV;
-        if (!(ok = mbar_wait_warp(&bar.k_empty[ks], ((cnt / C::NK) & 1) ^ 1, abort, p.status, site0 + 1))) break;
+      for (int m = 0; m < w.nc; ++m) {
+        const uint32_t ks = nk % C::NK, vs = nv % C::NV;
+        if (!(ok = mbar_wait_warp(&bar.k_empty[ks], ((nk / C::NK) & 1) ^ 1, abort, p.status, site0 + 1))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bar.k_full[ks], T::BYTES);
           swa_load_tile<D>(sbase + C::K_OFF + ks * T::TILE, &tmK, &tmK1, &bar.k_full[ks], swa_key(w, m), w.hk, w.b);
         }
         __syncwarp();
-        if (!(ok = mbar_wait_warp(&bar.v_empty[vs], ((cnt / C::NV) & 1) ^ 1, abort, p.status, site0 + 1))) {
-          ++cnt;       // (K was issued)
-          break;
-        }
+        ++nk;
+        if (!(ok = mbar_wait_warp(&bar.v_empty[vs], ((nv / C::NV) & 1) ^ 1, abort, p.status, site0 + 1))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bar.v_full[vs], T::BYTES);
           swa_load_tile<D>(sbase + C::V_OFF + vs * T::TILE, &tmV, &tmV1, &bar.v_full[vs], swa_key(w, m), w.hk, w.b);
         }
         __syncwarp();
+        ++nv;
       }
     }
-    if (*abort) {
-      drain_ring(bar.k_full, cnt, C::NK, p.status);
-      drain_ring(bar.v_full, cnt, C::NV, p.status);
-    }
+    drain_ring(bar.k_full, nk, C::NK, p.status);
+    drain_ring(bar.v_full, nv, C::NV, p.status);
   } else if (warp == 3) {
     // ------------------------------------------------------------ Q
     uint32_t cnt = 0;
@@ -217,7 +214,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       __syncwarp();
     }
-    if (*abort) drain_ring(bar.q_full, cnt, C::QS, p.status);
+    drain_ring(bar.q_full, cnt, C::QS, p.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S
     // Of each half chunk, once its slot's last probabilities have been consumed.
@@ -256,6 +253,7 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     swa_issued(&bar.mma_done[0], p.status);
   } else if (warp == 2) {
     // ------------------------------------------------------------ O += P V
+    const bool mute = swa_take_fault(p.status, 1);
     uint32_t step = 0, an = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < nitems; u += gridDim.x, ++an) {
@@ -276,10 +274,12 @@ swa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               swa_acc32<D>(tmem + C::O + D * (2 * x), tP, vt, 2 * x, m == 0);
               swa_acc32<D>(tmem + C::O + D * (2 * x + 1), tP + 32, vt, 2 * x + 1, m == 0);
             }
-            umma_commit(&bar.pv_done[x][sl]);
-            if (x == 1) {
-              umma_commit(&bar.v_empty[vs]);
-              if (m == w.nc - 1) umma_commit(&bar.o_full);
+            if (!mute || step > 0) {
+              umma_commit(&bar.pv_done[x][sl]);
+              if (x == 1) {
+                umma_commit(&bar.v_empty[vs]);
+                if (m == w.nc - 1) umma_commit(&bar.o_full);
+              }
             }
           }
           __syncwarp();

@@ -111,7 +111,8 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                : "memory");
 }
 
-// After an abort: waits (with the limit) until the last loads of a ring have landed.
+// The end of a loading warp: the last loads of each stage land (within the limit) before the
+// CTA can retire, also when the roles that wait for them have given up.  cnt: loads issued.
 __device__ __forceinline__ void drain_ring(uint64_t *full, uint32_t cnt, uint32_t stages, const int *status) {
   for (uint32_t u = cnt > stages ? cnt - stages : 0; u < cnt; ++u) {
     const unsigned long long t0 = global_timer_ns();
@@ -150,6 +151,16 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
 // Bits e and e + 1 of b as the halves of a packed pair.
 __device__ __forceinline__ uint32_t pair_mask(uint32_t b, int e) {
   return ((b >> e) & 1u ? 0x0000FFFFu : 0u) | ((b >> (e + 1)) & 1u ? 0xFFFF0000u : 0u);
+}
+
+// Test hook (moba_debug_fault_next_launch): the warp of CTA 0 that issues the accumulating
+// products takes the one-shot flag and does not announce its first products, so that a wait
+// for them runs out.  (This warp waits for its first operands anyway.)
+__device__ __forceinline__ bool swa_take_fault(int *status, int kind) {
+  if (blockIdx.x != 0) return false;
+  int mine = 0;
+  if ((threadIdx.x & 31) == 0) mine = atomicCAS(&status[3], kind, 0) == kind;
+  return __shfl_sync(0xffffffffu, mine, 0) != 0;
 }
 
 // The end of an issuing warp: everything it issued completes (within the wait limit)

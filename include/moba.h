@@ -399,10 +399,12 @@ int moba_device_status(void);
  * moba_debug_set_wait_limit_us: every kernel wait that has not completed after this
  *   many microseconds gives up (MOBA_ERR_DEVICE); 0 restores the default of 2 s.
  * moba_debug_fault_next_launch(1): the next attention launch (moba_attn_fwd's passes or
- *   swa_attn_fwd without sinks) leaves the first V chunk of its first CTA unloaded, so that a wait
- *   runs out on purpose: the launch ends through the bounded-wait path (its roles stop,
+ *   swa_attn_fwd without sinks) leaves the first V chunk of its first CTA unloaded, or (with
+ *   sinks; the dQ kernel of swa_attn_bwd) that CTA does not announce its first product, so that
+ *   a wait runs out on purpose: the launch ends through the bounded-wait path (its roles stop,
  *   copies in flight are drained, TMEM is freed) and moba_device_status() then reports
- *   MOBA_ERR_DEVICE.  One shot: the launch that takes the flag clears it; 0 clears it.
+ *   MOBA_ERR_DEVICE.  2: the same of the next dK / dV kernel of swa_attn_bwd.  One shot: the
+ *   launch that takes the flag clears it; 0 clears it.
  *   Nothing faults or traps, and the context stays usable.
  * Return MOBA_OK, MOBA_ERR_ARG for a value out of range, MOBA_ERR_LAUNCH when a CUDA call
  * fails.  The paper has no counterpart; these exist to test failure handling.

@@ -73,3 +73,38 @@ def test_a_wait_that_runs_out_is_not_hidden_by_a_bad_index(index_first):
     assert moba.device_status() == 0
     _bad_index(moba)
     assert moba.device_status() == -10 and moba.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("which", ["forward", "dq", "dkdv"])
+def test_the_sliding_window_kernels_give_up_in_one_wait(which, d):
+    """A product of the first CTA that is never announced: the launch ends after one wait limit
+    (a loader that gives up between two copies must not wait for the one it has not issued),
+    says so, and the next call is right to the bit."""
+    import block_sparse_long_prefill_b200 as moba
+    g = torch.Generator("cuda").manual_seed(d)
+    q, k, v, do = (torch.randn(1, h, 2000, d, generator=g, device="cuda").bfloat16() for h in (2, 1, 1, 2))
+
+    def fwd():
+        return moba.swa_attn_fwd(q, k, v, 1500, sink=4)
+
+    out, lse = fwd()
+    call = fwd if which == "forward" else lambda: moba.swa_attn_bwd(q, k, v, out, lse, do, 1500, 4)
+    want = call()
+    assert moba.device_status() == 0
+    limit = 0.05
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    try:
+        moba.debug_set_wait_limit_us(int(limit * 1e6))
+        moba.debug_fault_next_launch(2 if which == "dkdv" else 1)
+        start.record()
+        call()
+        end.record()
+        assert moba.device_status() == MOBA_ERR_DEVICE
+    finally:
+        moba.debug_fault_next_launch(0)
+        moba.debug_set_wait_limit_us(0)
+    # One limit, and the launches themselves (well below a millisecond).
+    assert limit <= start.elapsed_time(end) * 1e-3 < 1.5 * limit
+    assert all(torch.equal(a, b) for a, b in zip(want, call()))
+    assert moba.device_status() == 0
