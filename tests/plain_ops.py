@@ -65,6 +65,28 @@ def attention_bwd(q, k, v, do, see, scale=None, out_bound=None):
     return (dq, bq + FLUSH), (dk, bk + FLUSH), (dv, bv + FLUSH)
 
 
+def attention_bwd_norms(q, k, v, do, see, scale=None):
+    """How far the kernels' whole gradients may be from the formula's, in the 2-norm (dq, dk, dv).
+
+    Roundings to bf16 err by at most 2^-8 of the value and, value by value, with independent
+    signs, so their squares add up: of the stored result, of each dz (of each P for dv), and,
+    through D = dO.o, of the stored ``out`` and of the P behind it.  (Each is at its largest
+    here; a rounding's root mean square is less than half of it, which leaves room for the
+    float32 sums.)"""
+    scale = scale or q.shape[-1] ** -0.5
+    out, _, p, _, _ = attention(q, k, v, see, scale)
+    dp = do @ v.transpose(-1, -2)
+    dz = p * (dp - (do * out).sum(-1, keepdim=True))
+    dq, dk, dv = scale * dz @ k, scale * dz.transpose(-1, -2) @ q, p.transpose(-1, -2) @ do
+    derr2 = (do.square() * out.square()).sum(-1, keepdim=True) + (p * dp).square().sum(-1, keepdim=True)
+    dqn = dq.square().sum() + scale ** 2 * ((dz.square() @ k.square()).sum() + (derr2 * (p @ k).square()).sum())
+    # (A row's error in D reaches every key that it sees.)
+    dkn = dk.square().sum() + scale ** 2 * ((dz.square().transpose(-1, -2) @ q.square()).sum()
+                                            + (p.square().transpose(-1, -2) @ (derr2 * q.square())).sum())
+    dvn = dv.square().sum() + (p.square().transpose(-1, -2) @ do.square()).sum()
+    return tuple(BF16 * float(x) ** 0.5 for x in (dqn, dkn, dvn))
+
+
 def turn(x, cos, sin, interleaved, sign=1.0):
     """Rotation of the first 2 * cos.shape[-1] columns; returns the result and the sum of
     magnitudes behind each value."""

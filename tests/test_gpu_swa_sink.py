@@ -259,3 +259,75 @@ def test_forward_without_the_compiled_binding(monkeypatch):
         moba.swa_attn_fwd(q, k[:1], v, 77)
     with pytest.raises(ImportError):
         moba.swa_attn_bwd(q, q, q, q, lse, q, 77)
+
+
+@pytest.mark.parametrize("d,hq,hkv,n,nk,window", [(64, 2, 1, 900, 900, 200), (80, 2, 2, 333, 900, 128),
+                                                  (128, 4, 2, 900, 900, 200), (128, 2, 1, 700, 700, 5000)])
+def test_forward_of_the_band_alone(d, hq, hkv, n, nk, window):
+    """No sinks: the float64 band."""
+    _fwd(1, hq, hkv, n, nk, d, window, 0, seed=window)
+
+
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("hq,hkv,n,window,sink", [(2, 2, 1000, 1000, 0), (4, 2, 1100, 500, 4), (8, 2, 900, 130, 140),
+                                                  (2, 1, 700, 5, 1)])
+def test_whole_gradients(d, hq, hkv, n, window, sink):
+    """Each gradient as a whole: the bounds of single values add up magnitudes, which at wide
+    windows leaves room for errors of D or of the sums that the 2-norm does not."""
+    moba = _moba()
+    q, k, v, do = _inputs(2, hq, hkv, n, n, d, n + d)
+    out, lse = moba.swa_attn_fwd(q, k, v, window, sink=sink)
+    got = moba.swa_attn_bwd(q, k, v, out, lse, do, window, sink)
+    assert moba.device_status() == 0
+    G, see = hq // hkv, po.visible(n, n, window, sink, "cuda")
+    args = q.double(), _wide(k, G), _wide(v, G), do.double(), see
+    (wq, _), (wk, _), (wv, _) = po.attention_bwd(*args)
+    want = wq, wk.view(2, hkv, G, n, d).sum(2), wv.view(2, hkv, G, n, d).sum(2)
+    bounds = list(po.attention_bwd_norms(*args))
+    if G > 1:   # (stored once, after the sum over the heads: its rounding is of the sum)
+        bounds[1:] = [(b ** 2 + (po.BF16 * float(w.norm())) ** 2) ** 0.5 for b, w in zip(bounds[1:], want[1:])]
+    for name, x, w, b in zip(("dq", "dk", "dv"), got, want, bounds):
+        err = float((x.double() - w).norm())
+        assert err <= b, (name, err, b, float(w.norm()))
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_gradients_equal_differences_of_the_forward(name, d):
+    """sum(dO out) of the kernel's own forward, in a step along the kernel's gradient, where the
+    loss changes most: by many times what its roundings leave open."""
+    moba = _moba()
+    hq, hkv, n, window, sink = 2, 1, 300, 50, 3
+    x = dict(zip(("q", "k", "v", "do"), _inputs(1, hq, hkv, n, n, d, 5)))
+    do, see, scale = x["do"].double(), po.visible(n, n, window, sink, "cuda"), d ** -0.5
+    out, lse = moba.swa_attn_fwd(x["q"], x["k"], x["v"], window, sink=sink)
+    grads = dict(zip(("q", "k", "v"), moba.swa_attn_bwd(x["q"], x["k"], x["v"], out, lse, x["do"], window, sink)))
+
+    def plain(y):
+        """The loss in float64, and how far the kernel's may be from it: the stored out, P before
+        its product, and float32 scores and sums (2^-13 of the terms)."""
+        q, k, v = y["q"].double(), _wide(y["k"], hq // hkv), _wide(y["v"], hq // hkv)
+        o, _, p, _, _ = po.attention(q, k, v, see)
+        terms = (p * (do @ v.mT).abs()).sum()
+        return float((do * o).sum()), float(po.BF16 * ((do * o).abs().sum() + terms) + 2.0 ** -13 * terms)
+
+    def loss(y):
+        return float((moba.swa_attn_fwd(y["q"], y["k"], y["v"], window, sink=sink)[0].double() * do).sum())
+
+    g = grads[name].double()
+    step = dict(q=0.5, k=0.5, v=2.0)[name]
+    up, down = (dict(x, **{name: (x[name].double() + s * step * g).bfloat16()}) for s in (1, -1))
+    way = up[name].double() - down[name].double()
+    want = float((g * way).sum())
+    (lu, eu), (ld, ed) = plain(up), plain(down)
+    # The loss bends along q and k: the formula's difference misses its own gradient by as much.
+    args = x["q"].double(), _wide(x["k"], hq // hkv), _wide(x["v"], hq // hkv), do, see
+    exact = dict(zip("qkv", (w for w, _ in po.attention_bwd(*args))))[name]
+    if name != "q":
+        exact = exact.view(1, hkv, hq // hkv, n, d).sum(2)
+    want += lu - ld - float((exact * way).sum())
+    # The gradient itself: its whole error (twice the heads' norms) along the way.
+    norm = 2 * dict(zip("qkv", po.attention_bwd_norms(*args)))[name] * float(way.norm())
+    tol = eu + ed + norm
+    assert tol < 0.1 * want, (tol, want)
+    assert abs(loss(up) - loss(down) - want) <= tol, (loss(up) - loss(down), want, tol)

@@ -58,6 +58,30 @@ def test_attention_gradients(window, sink):
     _difference(lambda x: loss(q, k, x), v, dv)
 
 
+def _rounded_gradients(q, k, v, do, see, d_factor=1.0):
+    """The backward with the kernels' roundings, D taken ``d_factor`` times."""
+    r = lambda x: x.bfloat16().double()  # noqa: E731
+    scale = q.shape[-1] ** -0.5
+    z = (q @ k.mT * scale).masked_fill(~see, -math.inf)
+    p = torch.softmax(z, -1)
+    out = r(r(p) @ v)
+    dz = r(p * (do @ v.mT - d_factor * (do * out).sum(-1, keepdim=True)))
+    return r(scale * dz @ k), r(scale * dz.mT @ q), r(r(p).mT @ do)
+
+
+@pytest.mark.parametrize("n,window,sink", [(300, 300, 0), (300, 100, 4), (200, 2, 1), (500, 60, 130)])
+def test_gradients_with_the_kernels_roundings_are_within_their_norms(n, window, sink):
+    q, k, v, do = (_rand(2, n, 64, seed=i).bfloat16().double() for i in range(4))
+    see = po.visible(n, n, window, sink)
+    want = [g for g, _ in po.attention_bwd(q, k, v, do, see)]
+    bounds = po.attention_bwd_norms(q, k, v, do, see)
+    for got, w, b in zip(_rounded_gradients(q, k, v, do, see), want, bounds):
+        assert float((got - w).norm()) <= b <= 0.02 * float(w.norm())
+    # What D contributes to dq is not covered when it is off by a tenth.
+    off = _rounded_gradients(q, k, v, do, see, 1.1)
+    assert float((off[0] - want[0]).norm()) > bounds[0]
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("rot", [16, 24])
 def test_rotation_is_a_complex_product(interleaved, rot):
