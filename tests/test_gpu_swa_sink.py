@@ -331,3 +331,55 @@ def test_gradients_equal_differences_of_the_forward(name, d):
     tol = eu + ed + norm
     assert tol < 0.1 * want, (tol, want)
     assert abs(loss(up) - loss(down) - want) <= tol, (loss(up) - loss(down), want, tol)
+
+
+def test_backward_offsets_beyond_32_bits():
+    """The same sizes in the backward: the last rows and keys of the last heads, and the sinks'
+    keys, which every row of their sixteen heads sees."""
+    moba = _moba()
+    n, d, window, sink, hq, hkv = 1 << 20, 128, 128, 3, 32, 2
+    G, scale, m = hq // hkv, d ** -0.5, 400
+    g = torch.Generator("cuda").manual_seed(33)
+
+    def rand(heads):
+        x = torch.empty(1, heads, n, d, dtype=torch.bfloat16, device="cuda")
+        for h in range(heads):
+            x[0, h].copy_(torch.randn(n, d, generator=g, device="cuda"))
+        return x
+
+    q, do, k, v = rand(hq), rand(hq), rand(hkv), rand(hkv)
+    out, lse = moba.swa_attn_fwd(q, k, v, window, sink=sink)
+    dq, dk, dv = moba.swa_attn_bwd(q, k, v, out, lse, do, window, sink)
+    assert moba.device_status() == 0
+    # The last m - window rows of the last KV head's query heads against the keys that they see.
+    at = torch.cat([torch.arange(sink, device="cuda"), torch.arange(n - m, n, device="cuda")])
+    see = torch.cat([torch.ones(m, sink, dtype=torch.bool, device="cuda"), po.visible(m, m, window, 0, "cuda")], 1)
+    keep = m - window
+    kk, vv = (x[0, -1, at].double().expand(G, -1, -1) for x in (k, v))
+    args = q[0, -G:, -m:].double(), kk, vv, do[0, -G:, -m:].double(), see
+    o, _, _, ob, _ = po.attention(*args[:3], see)
+    (wq, bq), (wk, bk), (wv, bv) = po.attention_bwd(*args, None, ob)
+    po.check("dq", dq[0, -G:, -keep:], wq[:, -keep:], bq[:, -keep:])
+    # (Keys of the last window - 1 positions are seen by these rows alone, and by all of them.)
+    last = window - 1
+    po.check("dk", dk[0, -1, -last:], wk.sum(0)[-last:], bk.sum(0)[-last:])
+    po.check("dv", dv[0, -1, -last:], wv.sum(0)[-last:], bv.sum(0)[-last:])
+    for hk in (0, hkv - 1):
+        ks, vs = k[0, hk, :sink].double(), v[0, hk, :sink].double()
+        want, bound = ([torch.zeros(sink, d, dtype=torch.float64, device="cuda") for _ in range(2)] for _ in range(2))
+        for h in range(hk * G, (hk + 1) * G):
+            for a in range(0, n, n // 4):
+                rows = slice(a, a + n // 4)
+                qq, oo, gg = q[0, h, rows].double(), out[0, h, rows].double(), do[0, h, rows].double()
+                i = torch.arange(a, a + n // 4, device="cuda")
+                p = torch.exp(scale * qq @ ks.T - lse[0, h, rows].double()[:, None])
+                p = torch.where(i[:, None] >= torch.arange(sink, device="cuda"), p, 0.0)
+                dz = p * (gg @ vs.T - (gg * oo).sum(-1, keepdim=True))
+                for x, y, w in ((want[0], bound[0], (dz, qq, scale)), (want[1], bound[1], (p, gg, 1.0))):
+                    x += w[2] * w[0].T @ w[1]
+                    # (Every dz and P is rounded, and the squares of the errors add up; D is the one
+                    # that the kernel takes, float32 statistics and sums err by far less.)
+                    y += (w[2] * po.BF16) ** 2 * w[0].square().T @ w[1].square()
+        for name, x, w, b in (("dk", dk, want[0], bound[0]), ("dv", dv, want[1], bound[1])):
+            err = x[0, hk, :sink].double() - w
+            assert float(err.norm()) <= float((b.sum() + (po.BF16 * w).square().sum()).sqrt()), (name, hk)
