@@ -279,7 +279,8 @@ def moba_attn_fwd(q, k, v, idx, block: int, topk: int, workspace: torch.Tensor, 
 def swa_attn_fwd(q, k, v, window: int, scale: float = 0.0, out=None, lse=None, stream=None,
                  sink: int = 0):
     """[SWA] §슬라이딩 윈도우 마스크: causal band attention (window >= N is dense causal),
-    the first ``sink`` tokens staying visible behind the window."""
+    the first ``sink`` tokens staying visible behind the window.  k and v must be finite also
+    where no row sees them (padding): hidden values are multiplied by zero."""
     return swa_attn_fwd_chunk(q, k, v, window, scale, out, lse, stream, sink)
 
 
@@ -381,7 +382,7 @@ def swa_bwd_workspace_size(batch, hq, hkv, N, d, window, sink=0) -> int:
 def swa_attn_bwd(q, k, v, out, lse, dout, window: int, sink: int = 0, scale: float = 0.0, dq=None,
                  dk=None, dv=None, workspace=None, stream=None):
     """Gradients of swa_attn_fwd (``window``, ``sink`` and ``scale`` as given to it) for whole
-    sequences.  Returns (dq, dk, dv), bf16."""
+    sequences.  q, k, v and dout must be finite.  Returns (dq, dk, dv), bf16."""
     stream = _own_stream("swa_attn_bwd", stream, q)
     with _on_stream(stream):
         rc, dq, dk, dv = _binding.swa_bwd(q, k, v, out, lse, dout, window, sink, scale, dq, dk, dv, workspace)
@@ -431,8 +432,9 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, cos
     j % page of page page_table[b, j // page].  seq_lens int32 [batch]: lengths with the new
     tokens, which are a sequence's last; cu_seqlens int32 [batch + 1] on the device: sequence
     b's tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (default: one token a sequence).
-    With q [T, hq, d], returns the queries normalised and rotated to the same positions
-    (tokens behind the last sequence are left as they were), else None."""
+    With q [T, hq, d], returns the queries normalised and rotated to the same positions, else
+    None.  Tokens behind the last sequence, and those whose position or page is not there
+    (device_status), are left as they were in the pages and in q_out."""
     stream = _own_stream("kv_append", stream, k)
     with _on_stream(stream):
         rc, q_out = _binding.append(k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, cos, sin, k_weight,

@@ -5,8 +5,8 @@
 //     out = softmax(scale q K^T) V over these keys, lse = log sum exp(scale q k).
 // Position j lies in slot j % page of page table[b, j / page].
 //
-// Every visible key and value is read once and used for the G query heads of its KV head,
-// so the work is HBM-bound (4 G flops a byte at most).  The keys of a (sequence, KV head,
+// Every visible key and value is read once for each group of up to 16 of the G query heads of
+// its KV head, so the work is HBM-bound (up to 16 flops a byte).  The keys of a (sequence, KV head,
 // group of up to 16 query heads) -- an item -- are cut into tiles of 16, and the work of
 // the batch is dealt out in equal runs to a grid of two or three CTAs per SM, whatever the
 // sequences' lengths: a run may end inside an item, which then has partial results
@@ -14,8 +14,9 @@
 // as its tiles and kDecItem more, about what filling the pipeline and joining the warps
 // costs: by tiles alone a run of many one-tile items took six times as long as one of few
 // long items (32 ragged sequences of 32 heads with a window of 4096: 237 against 88 us).
-// Measured: one sequence of 2^20 tokens, 8 KV heads of 128, 683 us with the call, 6.3 TB/s;
-// 48 ragged sequences of up to 16384 tokens 90 us, 5.1 TB/s (fills and ends of 384 items).
+// Measured: one sequence of 2^20 tokens, 8 KV heads of 128, 683 us with the call, 6.3 TB/s
+// (746 us, 5.8 TB/s on a card with a slower memory); 48 ragged sequences of up to 16384 tokens
+// 90 us, 5.1 TB/s (fills and ends of 384 items; 95 us on the other card).
 //
 // A warp takes every fourth tile of its CTA's run and works alone: its tiles arrive by
 // cp.async in a ring of its own (three stages of 16 keys and 16 values, about 9 KB each,
@@ -23,8 +24,9 @@
 // needs over the memory's latency), page ids are read a tile ahead, and S = Q K^T and
 // O += P V run on mma.sync m16n8k16 (query heads as the 16 rows; a tensor pipe at a few
 // per cent, so the wider tcgen05 tiles would only idle).  The softmax is one pass with a
-// running maximum and sum in fp32; P is rounded to bf16 for the product (half a step,
-// 2^-9 relative, less than the rounding of the output).  The four warps' results are
+// running maximum and sum in fp32; P is rounded to bf16 for the product, as in the prefill (up
+// to 2^-8 of each value, the same step as the output's own; the output is off by 0.0015 to
+// 0.0022 of its norm, 0.0013 to 0.0016 of them its own rounding).  The four warps' results are
 // joined through shared memory at the end of an item.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -18,9 +18,11 @@
 // In the half layout a column's partner sits in another lane's vector: four shuffles of
 // packed bf16 pairs fetch it, and the row sums are a butterfly of the same lanes.
 // Measured: forward of 32768 tokens, 32 and 8 heads of 128, 125 us (5.4 TB/s); append of
-// 4 ragged chunks of up to 4096 tokens, 32 KV heads of 80, 38.5 us (5.3 TB/s); backward of 2 x 8191 tokens, 32 and
+// 4 ragged chunks of up to 4096 tokens, 32 KV heads of 80, 37.5 us (5.5 TB/s), of one token of
+// 64 sequences, 32 and 8 heads of 128, 3.5 us in a graph; backward of 2 x 8191 tokens, 32 and
 // 8 heads of 128, 122 us (4.1 TB/s): its arithmetic, 230 instructions a warp and row group,
-// and its registers (2 CTAs an SM; 3 spill, 297 us) bound it as much as HBM does.
+// and its registers (2 CTAs an SM; 3 spill, 297 us) bound it as much as HBM does.  Without
+// norms (all 128 columns turned, halves) 80 us, 4.3 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
       for (int e = 0; e < 4; ++e) dw.v[e] = make_float2(0.f, 0.f);
     }
     // Rounds in pairs: a warp takes the rounds 2 k, 2 k + 1 for k = gw, gw + nw, ...
-    // (Fewer than 2^30 by the call's check.)
+    // (Below 2^32 - 2^14 by the call's check, so that the steps cannot pass the end.)
     const unsigned rounds = (unsigned)chunks * (unsigned)groups * (unsigned)p.batch;
     auto after = [&](unsigned k) { return (k & 1) ? k + 2u * nw - 1u : k + 1u; };
     struct Round {

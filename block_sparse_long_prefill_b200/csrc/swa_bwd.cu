@@ -22,9 +22,12 @@
 //                         times as long, so theirs are cut into parts that leave fp32 sums
 //   swa_bwd_join_kernel   adds the parts of the sinks' key tiles, in order; latency-bound
 //
-// P and dz are rounded to bf16 for their products (half a step, 2^-9 of each value; gradients
-// are then off by 0.0024 of their norm, against 0.0017 by the rounding of the results alone);
-// sums, statistics and accumulators are fp32.  D takes `out` as it was returned, in bf16.
+// P and dz are rounded to bf16, their products' operand type (two terms of each would double
+// three of the five products): up to 2^-8 of each value, the same step as the results'; gradients
+// are then off by 0.0024 of their norm, against 0.0017 by the rounding of the results alone.
+// Sums, statistics and accumulators are fp32.  D takes `out` as it was returned, in bf16, so that
+// the forward writes nothing more: where one or two keys hold a row, dP - D cancels and gradients
+// are off by 0.003 to 0.006.
 //
 // Both tile kernels compute S and dP again (7 products instead of 5): a single pass would
 // have to add dQ in global memory from every key tile, in an order that varies.  They are
