@@ -379,17 +379,17 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (D != 64) tma_load_4d(dst + C::R0, m1, &full[st], 64, key, w.hk, w.b);
           }
         }
-        // Let every load issued so far land before the CTA can retire.
-        if (*abort) {
-          for (uint32_t u = (cnt > (uint32_t)C::ST ? cnt - C::ST : 0); u < cnt; ++u) {
-            const unsigned long long t0 = global_timer_ns();
-            while (!mbar_try_wait(&full[u % C::ST], (u / C::ST) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
-          }
-          for (int x = 0; x < 2; ++x) {
-            if (quse[x] == 0) continue;
-            const unsigned long long t0 = global_timer_ns();
-            while (!mbar_try_wait(&bar.q_full[x], (quse[x] - 1) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
-          }
+        // Let every load issued so far land before the CTA can retire, also when the roles
+        // that wait for them give up later than this one ends.
+        for (uint32_t u = (cnt > (uint32_t)C::ST ? cnt - C::ST : 0); u < cnt; ++u) {
+          if (skip_first && u == 0) continue;
+          const unsigned long long t0 = global_timer_ns();
+          while (!mbar_try_wait(&full[u % C::ST], (u / C::ST) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
+        }
+        for (int x = 0; x < 2; ++x) {
+          if (quse[x] == 0) continue;
+          const unsigned long long t0 = global_timer_ns();
+          while (!mbar_try_wait(&bar.q_full[x], (quse[x] - 1) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
         }
       }
     } else if (warp == 1) {
@@ -535,8 +535,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (tx.rows > 0) rows_of(tx, rr, true);
           }
         }
-        // After an abort, let the last gather land before the CTA can retire.
-        if (*abort && quse > 0) {
+        // Let the last gather land before the CTA can retire.
+        if (quse > 0) {
           const unsigned long long t0 = global_timer_ns();
           while (!mbar_try_wait(&bar.q_full[x], (quse - 1) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
         }

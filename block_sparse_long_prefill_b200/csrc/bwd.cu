@@ -369,11 +369,10 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
           if (D == 128) tma_load_4d(dst + T::R0, m, &full[st], 64, key, it.hk, it.b);
         }
       }
-      if (*abort) {
-        for (uint32_t u = (cnt > (uint32_t)C::ST ? cnt - C::ST : 0); u < cnt; ++u) {
-          const unsigned long long t0 = global_timer_ns();
-          while (!mbar_try_wait(&full[u % C::ST], (u / C::ST) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
-        }
+      // Every load issued lands before the CTA can retire, whoever gives up.
+      for (uint32_t u = (cnt > (uint32_t)C::ST ? cnt - C::ST : 0); u < cnt; ++u) {
+        const unsigned long long t0 = global_timer_ns();
+        while (!mbar_try_wait(&full[u % C::ST], (u / C::ST) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
       }
     }
   } else if (warp == 1) {
@@ -750,7 +749,7 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           tma_load_4d(vd + T::R0, &tmV, &bar.k_full[0], 64, w.kt0, w.hk, w.b);
         }
       }
-      if (*abort && kn > 0) {
+      if (kn > 0) {   // (lands before the CTA can retire, whoever gives up)
         const unsigned long long t0 = global_timer_ns();
         while (!mbar_try_wait(&bar.k_full[0], (kn - 1) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
       }

@@ -411,8 +411,8 @@ gate_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         ++quse;
       }
       }
-      if (*abort) {
-        // Let issued loads land before the CTA can retire.
+      {
+        // Let issued loads land before the CTA can retire, whoever gives up.
         const unsigned long long t0 = global_timer_ns();
         for (uint32_t u = (quse > (uint32_t)qst ? quse - qst : 0u); u < quse; ++u)
           while (!mbar_try_wait(&bar.q_full[u % qst], (u / qst) & 1) && global_timer_ns() - t0 < wait_limit_ns(p.status)) {}
