@@ -13,7 +13,8 @@ Every call runs on the current stream of its tensors' device, or on ``stream``: 
 caller orders it behind what made the inputs and before what reads the results
 (``wait_stream``), as with any torch stream.  The calls around the attention (and
 swa_attn_fwd) keep the memory of inputs and results until both streams are done with it, so
-either may be dropped at any time.
+either may be dropped at any time; on a stream of another library's (an ExternalStream, an
+object with a ``cuda_stream``) the inputs and given results are the caller's to keep until then.
 
 Method sources (by page title and section):
   [MoBA] "MoBA: 어텐션에 전문가 혼합을 적용해 긴 문맥을 효율적으로 처리하는 블록 어텐션
@@ -225,11 +226,14 @@ def _hand_over(stream, inputs, results):
     """What a call on ``stream`` takes and gives belongs to two streams: the inputs (and results
     that were given) may be dropped by a caller on its own stream before the kernels are done
     with them, and results allocated on ``stream`` with work of the caller's still to come.
-    Their memory is not handed out again before both streams have finished.  (None: one stream.)"""
+    Their memory is not handed out again before both streams have finished.  (None: one stream.)
+    A stream that torch does not own may be gone when that memory is freed, and is not recorded:
+    there inputs and given results are the caller's to keep."""
     if stream is not None:
-        for t in (*inputs, *results):
-            if t is not None:
-                t.record_stream(stream)
+        if not isinstance(stream, torch.cuda.ExternalStream):
+            for t in (*inputs, *results):
+                if t is not None:
+                    t.record_stream(stream)
         for t in results:
             if t is not None:
                 t.record_stream(torch.cuda.current_stream(t.device))

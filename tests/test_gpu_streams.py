@@ -128,3 +128,72 @@ def test_given_results_stay_until_they_are_written():
     junk = [torch.full_like(x["q"], 9) for _ in range(3)]
     torch.cuda.synchronize()
     assert all((t == 9).all() for t in junk)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_stream_of_another_library_may_go_before_the_tensors(name):
+    """Its handle is invalid by the time the inputs and results are freed: nothing of torch's may
+    still refer to it."""
+    import ctypes
+    x, call = CALLS[name]()
+    want = call(x)
+    torch.cuda.synchronize()
+    rt, handle = torch.cuda.cudart(), ctypes.c_void_p()
+    assert int(rt.cudaStreamCreate(ctypes.addressof(handle))) == 0
+
+    class Theirs:
+        cuda_stream = handle.value
+
+    copies = {n: t.clone() for n, t in x.items()}
+    torch.cuda.synchronize()
+    got = call(copies, stream=Theirs())
+    torch.cuda.synchronize()
+    assert int(rt.cudaStreamDestroy(handle.value)) == 0
+    assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(want, got))
+    copies.clear()
+    del got
+    torch.cuda.synchronize()
+    again = [t.clone() for t in x.values()]
+    assert _moba().device_status() == 0 and again
+
+
+def test_the_default_stream_by_its_handle():
+    """Handle 0, from within another stream."""
+    x, call = CALLS["decode"]()
+    want = call(x)
+
+    class Default:
+        cuda_stream = 0
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = call(x, stream=Default())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "append"])   # (its helper waits on the host)
+def test_on_a_forked_stream_in_a_graph(name):
+    """Captured on a stream of its own, with inputs made and dropped within the capture."""
+    x, call = CALLS[name]()
+    want = call(x)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        copies = {n: t.clone() for n, t in x.items()}
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(copies, stream=side)
+        copies.clear()
+        junk = [torch.full_like(t, 1) for t in x.values() for _ in range(2)]
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            if t is not None:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(want, got))
+    del got, junk
+    torch.cuda.synchronize()
+    again = [t.clone() for t in x.values()]
+    assert _moba().device_status() == 0 and again
